@@ -1,0 +1,595 @@
+// attend.cuh — attention of a batch over a shared prefix and each sequence's
+// own tokens, both in the paged FP8 cache of rope.cuh.
+//
+//   row (token t of sequence b, query head h), KV head h / G:
+//     z_j = scale * (q . dec(K_j)) * sk_j   over the tokens the row sees: the
+//           P prefix tokens, and own tokens p < kv_len[b] - n_b + (t - t_b) + 1
+//           (its n_b new tokens are the last of its kv_len[b] cached ones)
+//     out = sum_j e^(z_j - lse) sv_j dec(V_j),   lse = ln sum_j e^(z_j)
+//   a row that sees nothing gets zeros and lse = -inf.
+//
+// The prefix is read once for the whole batch: the query rows of all
+// sequences that share a KV head (T * G of them) form the rows of one
+// matrix.  Both parts are cut along the tokens into chunks; each chunk's
+// normalised output and log-sum-exp go to the workspace in fp32, and
+// join_kernel weighs them together.
+//
+// attend_rows_kernel: row tiles of 16 on mma.sync (f16 operands, fp32 sums).
+// It serves the calls that are bound by reading the cache (a decode step's
+// own tokens: G rows per KV head), where a 128-row tcgen05 tile would be
+// almost empty.  e4m3 codes are exact in f16.  Q goes to f16 with a power of two per
+// row that puts its largest element in [2^7, 2^8): exact for elements down
+// to 2^-22 of that largest, off by at most 2^-33 of it below.  The
+// probabilities times the value scales go to f16 relative to the largest
+// value scale seen (a power of two M per warp): p sv / M 2^14, 11 bits down
+// to 2^-28 of M.  Sums, maxima and outputs stay in fp32.
+//
+// Each warp streams its own share of the chunk, 32 tokens at a time, through
+// a ring of three cp.async stages of its own, so warps never wait for one
+// another until they merge at the end.  The dot products' summation order is
+// free, so each lane's operand fragments are whole 16-byte pieces of code
+// rows: the four lanes of a quad take 16 (of each 64) dimensions of a key
+// row, and the eight lanes of a column group take 16 dimensions each of four
+// value rows, whose bytes are paired by token with byte permutes.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ptx.cuh"
+#include "quant.cuh"
+
+namespace mfp8 {
+namespace attend {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 16;    // query rows per tile
+constexpr int kIter = 32;    // tokens per warp and iteration
+constexpr int kStages = 3;
+constexpr int kMinChunk = kWarps * kIter * 2;  // tokens: below two iterations per warp a split costs more than it saves
+constexpr int64_t kMaxTokens = int64_t(1) << 30;  // of one sequence
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Params {
+    const __nv_bfloat16* Q;
+    int64_t ldq;  // elements between tokens
+    const int32_t* q_start;
+    int B, T, Hq, Hkv, G;
+    const uint8_t* K;
+    const float* k_scale;
+    const uint8_t* V;
+    const float* v_scale;
+    int64_t n_pages;
+    int ps_shift;
+    const int32_t* prefix_pages;
+    int prefix_len;
+    const int32_t* table;
+    int64_t ld_table;
+    int max_pages;
+    const int32_t* kv_len;
+    float scale_log2;  // softmax scale times log2(e)
+    __nv_bfloat16* O;  // [T][Hq][D]
+    float* lse;        // [T][Hq] or null
+    float* part;       // [slots][T * Hq][D], normalised partial outputs
+    float* part_lse;   // [slots][T * Hq], log2
+    int splits_p, splits_o;  // slots of the prefix, then of the own tokens
+    int tiles_p, tiles_o;    // row tiles
+    int max_q;
+    bool direct;  // one slot in all: write O and lse
+};
+
+// What a block of query rows attends to.
+struct Task {
+    int tok0;    // first token of the sequence (or batch)
+    int n;       // its tokens
+    int len;     // cached tokens
+    int offset;  // row r sees tokens below offset + r / G (own) or len (prefix)
+    bool prefix;
+    const int32_t* pages;
+    int slot0, splits;
+};
+
+__device__ __forceinline__ Task prefix_task(const Params& p) {
+    Task k;
+    const int q0 = min(max(p.q_start[0], 0), p.T);
+    k.tok0 = q0;
+    k.n = min(max(p.q_start[p.B], q0), p.T) - q0;
+    k.len = p.prefix_len;
+    k.offset = p.prefix_len;
+    k.prefix = true;
+    k.pages = p.prefix_pages;
+    k.slot0 = 0;
+    k.splits = p.splits_p;
+    return k;
+}
+
+// Device lengths that do not fit what the call said are cut and reported.
+__device__ __forceinline__ Task own_task(const Params& p, int b) {
+    Task k;
+    const int a = p.q_start[b], e = p.q_start[b + 1], l = p.kv_len[b];
+    const int q0 = min(max(a, 0), p.T);
+    const int q1 = min(max(e, q0), p.T);
+    const int most = int(min(int64_t(p.max_pages) << p.ps_shift, kMaxTokens));
+    k.tok0 = q0;
+    k.n = min(q1 - q0, p.max_q);
+    k.len = min(max(l, 0), most);
+    if (a != q0 || e != q1 || k.n != q1 - q0 || l != k.len) record_device_status(MFP8_ERR_INDEX);
+    k.offset = k.len - (q1 - q0) + 1;
+    k.prefix = false;
+    k.pages = p.table + int64_t(b) * p.ld_table;
+    k.slot0 = p.splits_p;
+    k.splits = p.splits_o;
+    return k;
+}
+
+__device__ __forceinline__ int visible(const Task& k, int token) {
+    return k.prefix ? k.len : min(k.len, k.offset + token);
+}
+
+// Page index of token `tok` of the task, checked against the pool.
+__device__ __forceinline__ int page_of(const Params& p, const Task& k, int tok, int last) {
+    const int pg = __ldg(k.pages + (min(tok, last) >> p.ps_shift));
+    if (uint32_t(pg) >= uint64_t(p.n_pages)) {
+        record_device_status(MFP8_ERR_INDEX);
+        return 0;
+    }
+    return pg;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t f16x2_of_codes(uint16_t codes2) {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(codes2));
+    return h2;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+
+// The exponent that scales row values into [2^7, 2^8) from the largest
+// magnitude's bf16 bits (tiny rows are taken as 2^-119).
+__device__ __forceinline__ int row_exponent(uint32_t amax_bits) { return max(int(amax_bits >> 7), 8) - 127 - 7; }
+
+template <int D>
+struct RowsLayout {
+    static constexpr int CHUNKS = D / 16;                 // 16-byte pieces of a code row
+    static constexpr int STAGE = 2 * kIter * D + 2 * kIter * 4;  // K, V, k_scale, v_scale
+    static constexpr int RING = kStages * STAGE;
+    static constexpr int OPITCH = D + 4;
+    static constexpr int MERGE = kWarps * kRows * OPITCH * 4 + kWarps * kRows * 4;
+    static constexpr int SMEM = kWarps * RING > MERGE ? kWarps * RING : MERGE;
+};
+
+// Piece `ch` of row r sits at piece ch ^ swz(r): a quad's key reads (rows r,
+// r + 1) and a column group's value reads (rows 2c + u, pieces g, g + 1)
+// each touch every bank once per eight lanes (D = 128).
+template <int D>
+__device__ __forceinline__ uint32_t swz(uint32_t r) {
+    return ((r & 6u) ^ ((r & 1u) << 2)) & uint32_t(D / 16 - 1);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+attend_rows_kernel(const Params p) {
+    using L = RowsLayout<D>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, c = lane & 3;
+
+    // ---- which rows, which tokens
+    int64_t u = blockIdx.x;
+    const int64_t np = int64_t(p.tiles_p) * p.splits_p * p.Hkv;
+    int split, h, tile;
+    Task k;
+    if (u < np) {
+        h = int(u % p.Hkv);
+        u /= p.Hkv;
+        split = int(u % p.splits_p);
+        tile = int(u / p.splits_p);
+        k = prefix_task(p);
+    } else {
+        u -= np;
+        h = int(u % p.Hkv);
+        u /= p.Hkv;
+        split = int(u % p.splits_o);
+        u /= p.splits_o;
+        tile = int(u % p.tiles_o);
+        k = own_task(p, int(u / p.tiles_o));
+    }
+    const int nrows = k.n * p.G;
+    const int r0 = tile * kRows;
+    if (r0 >= nrows) return;
+    const int rlast = min(r0 + kRows, nrows) - 1;
+    const int seen = max(visible(k, rlast / p.G), 0);  // of the tile's last row, which sees most
+    // Chunks of whole iterations of all warps; every chunk but the last is full.
+    int chunk = (k.len + k.splits - 1) / k.splits;
+    chunk = max((chunk + kWarps * kIter - 1) / (kWarps * kIter) * (kWarps * kIter), kMinChunk);
+    const int64_t first = int64_t(split) * chunk;
+    const int slot = k.slot0 + split;
+    if (first >= seen) {  // nothing here
+        for (int i = threadIdx.x; i < kRows; i += kThreads) {
+            const int r = r0 + i;
+            if (r < nrows) {
+                const int64_t row = int64_t(k.tok0 + r / p.G) * p.Hq + h * p.G + r % p.G;
+                if (!p.direct) p.part_lse[int64_t(slot) * p.T * p.Hq + row] = -INFINITY;
+                else if (p.lse) p.lse[row] = -INFINITY;
+            }
+        }
+        if (p.direct)
+            for (int i = threadIdx.x; i < kRows * (D / 8); i += kThreads) {
+                const int r = r0 + i / (D / 8);
+                if (r < nrows) {
+                    const int64_t row = int64_t(k.tok0 + r / p.G) * p.Hq + h * p.G + r % p.G;
+                    reinterpret_cast<uint4*>(p.O)[row * (D / 8) + i % (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+        return;
+    }
+    const int k0 = int(first), k1 = min(k0 + chunk, seen);
+    const int iters = (k1 - k0 + kIter - 1) / kIter;
+
+    // ---- the ring
+    const uint32_t ring = smem_u32(smem) + warp * L::RING;
+    auto load = [&](int it, int page) {  // `page`: of token 8 * (lane & 3) of the iteration
+        const uint32_t st = ring + uint32_t((it / kWarps) % kStages) * L::STAGE;
+        const int base = k0 + it * kIter;
+        constexpr int RPI = 32 / L::CHUNKS;  // rows per instruction
+        const int ch = lane % L::CHUNKS;
+        const int psm = (1 << p.ps_shift) - 1;
+#pragma unroll
+        for (int i = 0; i < kIter / RPI; ++i) {
+            const int r = i * RPI + lane / L::CHUNKS;
+            const int pg = __shfl_sync(0xffffffffu, page, (i * RPI) >> 3);
+            const int64_t at = (((int64_t(pg) * p.Hkv + h) << p.ps_shift) + ((base + r) & psm)) * D + ch * 16;
+            const uint32_t n = base + r < k1 ? 16u : 0u;  // rows past the end are filled with zeros
+            const uint32_t dst = st + r * D + ((ch ^ swz<D>(r)) << 4);
+            cp_async16(dst, p.K + at, n);
+            cp_async16(dst + kIter * D, p.V + at, n);
+        }
+        const int pg = __shfl_sync(0xffffffffu, page, lane >> 3);
+        const int64_t at = ((int64_t(pg) * p.Hkv + h) << p.ps_shift) + ((base + lane) & psm);
+        const uint32_t n = base + lane < k1 ? 4u : 0u;
+        cp_async4(st + 2 * kIter * D + lane * 4, p.k_scale + at, n);
+        cp_async4(st + 2 * kIter * D + kIter * 4 + lane * 4, p.v_scale + at, n);
+    };
+    auto page_at = [&](int it) { return it < iters ? page_of(p, k, k0 + it * kIter + 8 * c, k1 - 1) : 0; };
+
+    int next = warp;  // next iteration to load
+    int page = page_at(next);
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        const int page2 = page_at(next + kWarps);
+        if (next < iters) load(next, page);
+        cp_async_commit();
+        next += kWarps;
+        page = page2;
+    }
+
+    // ---- Q fragments: word w of a lane's codes is dimensions
+    // (w / 4) * 64 + c * 16 + (w % 4) * 4 .. + 3 of the row
+    constexpr int W = D / 16;
+    uint32_t qf[W][4];
+    float f[2];
+    int lim[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int r = r0 + g + 8 * half;
+        const bool live = r < nrows;
+        const int t = live ? r / p.G : 0;
+        const uint4* q = reinterpret_cast<const uint4*>(p.Q + int64_t(k.tok0 + t) * p.ldq +
+                                                        int64_t(h * p.G + (live ? r % p.G : 0)) * D + c * 16);
+        uint32_t w[W][2];
+        uint32_t acc = 0;
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+            const uint4 a = live ? q[i * 8] : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 b = live ? q[i * 8 + 1] : make_uint4(0u, 0u, 0u, 0u);
+            acc = absmax_bits_u4(b, absmax_bits_u4(a, acc));
+            w[4 * i][0] = a.x, w[4 * i][1] = a.y, w[4 * i + 1][0] = a.z, w[4 * i + 1][1] = a.w;
+            w[4 * i + 2][0] = b.x, w[4 * i + 2][1] = b.y, w[4 * i + 3][0] = b.z, w[4 * i + 3][1] = b.w;
+        }
+        uint32_t amax = max(acc & 0xffffu, acc >> 16);
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const int e = row_exponent(amax);
+        const float m = pow2i(-e);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            qf[i][half] = pack_f16x2(bf16_lo(w[i][0]) * m, bf16_hi(w[i][0]) * m);
+            qf[i][2 + half] = pack_f16x2(bf16_lo(w[i][1]) * m, bf16_hi(w[i][1]) * m);
+        }
+        f[half] = p.scale_log2 * pow2i(e);
+        lim[half] = live ? min(visible(k, t), k1) : 0;
+    }
+    const int all_see = k.prefix ? k1 : min(visible(k, r0 / p.G), k1);  // tokens below are seen by every row
+
+    // ---- the pass over the tokens
+    constexpr int NT = D / 8;  // column tiles of the output
+    float o[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    int vexp = 27;  // biased exponent just above the largest value scale seen, at least 2^-100
+
+    for (int it = warp; it < iters; it += kWarps) {
+        cp_async_wait<kStages - 2>();
+        __syncwarp();
+        const uint32_t st = ring + uint32_t((it / kWarps) % kStages) * L::STAGE;
+        const int base = k0 + it * kIter;
+        // z for 4 tiles of 8 tokens
+        float z[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            z[j][0] = z[j][1] = z[j][2] = z[j][3] = 0.0f;
+            const int r = j * 8 + g;
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+                const uint4 code = lds128(st + r * D + (((c + 4 * i) ^ swz<D>(r)) << 4));
+                const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    mma_f16(z[j], qf[4 * i + e], f16x2_of_codes(uint16_t(w[e] & 0xffffu)),
+                            f16x2_of_codes(uint16_t(w[e] >> 16)));
+            }
+        }
+        float2 sv[4];
+        float mx[2] = {-INFINITY, -INFINITY};
+        const bool masked = base + kIter > all_see;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t at = st + 2 * kIter * D + (j * 8 + 2 * c) * 4;
+            const uint2 a = lds64(at), b = lds64(at + kIter * 4);
+            sv[j] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+            const float ka = __uint_as_float(a.x), kb = __uint_as_float(a.y);
+            z[j][0] *= ka * f[0];
+            z[j][1] *= kb * f[0];
+            z[j][2] *= ka * f[1];
+            z[j][3] *= kb * f[1];
+            if (masked) {
+                const int t = base + j * 8 + 2 * c;
+                if (t >= lim[0]) z[j][0] = -INFINITY;
+                if (t + 1 >= lim[0]) z[j][1] = -INFINITY;
+                if (t >= lim[1]) z[j][2] = -INFINITY;
+                if (t + 1 >= lim[1]) z[j][3] = -INFINITY;
+            }
+            mx[0] = fmaxf(mx[0], fmaxf(z[j][0], z[j][1]));
+            mx[1] = fmaxf(mx[1], fmaxf(z[j][2], z[j][3]));
+        }
+        // largest value scale of the 32 tokens, as a power of two above it
+        const uint32_t svb = __reduce_max_sync(0xffffffffu, __float_as_uint(ld_shared_f32(st + 2 * kIter * D + kIter * 4 + lane * 4)));
+        const int ve = max(vexp, min(int(svb >> 23) + 1, 254));
+        const float vadj = pow2i(max(vexp - ve, -126));
+        const float vnorm = pow2i(14 - (ve - 127));
+        vexp = ve;
+        float keep[2], mm[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 1));
+            mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 2));
+            const float mn = fmaxf(m[half], mx[half]);
+            mm[half] = mn == -INFINITY ? 0.0f : mn;  // nothing seen yet: every term is e^-inf = 0
+            keep[half] = ex2(m[half] - mm[half]);
+            m[half] = mn;
+            l[half] *= keep[half];
+            keep[half] *= vadj;
+        }
+        if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                o[i][0] *= keep[0];
+                o[i][1] *= keep[0];
+                o[i][2] *= keep[1];
+                o[i][3] *= keep[1];
+            }
+        }
+        uint32_t pf[2][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float a0 = ex2(z[j][0] - mm[0]), a1 = ex2(z[j][1] - mm[0]);
+            const float b0 = ex2(z[j][2] - mm[1]), b1 = ex2(z[j][3] - mm[1]);
+            l[0] += a0 + a1;
+            l[1] += b0 + b1;
+            const float s0 = sv[j].x * vnorm, s1 = sv[j].y * vnorm;
+            pf[j >> 1][(j & 1) * 2] = pack_f16x2(a0 * s0, a1 * s1);
+            pf[j >> 1][(j & 1) * 2 + 1] = pack_f16x2(b0 * s0, b1 * s1);
+        }
+        // output: column tile i of lane group g is dimension g * NT + i
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            uint32_t a[4][NT / 4];  // value rows 2c, 2c + 1 of token tiles 2s and 2s + 1
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int r = (2 * s + (q >> 1)) * 8 + 2 * c + (q & 1);
+                const uint32_t row = st + kIter * D + r * D;
+                if constexpr (D == 128) {
+                    const uint4 v = lds128(row + ((g ^ swz<D>(r)) << 4));
+                    a[q][0] = v.x, a[q][1] = v.y, a[q][2] = v.z, a[q][3] = v.w;
+                } else {
+                    const uint2 v = lds64(row + (((g >> 1) ^ swz<D>(r)) << 4) + (g & 1) * 8);
+                    a[q][0] = v.x, a[q][1] = v.y;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < NT / 4; ++q) {
+                const uint32_t lo0 = __byte_perm(a[0][q], a[1][q], 0x5140), hi0 = __byte_perm(a[0][q], a[1][q], 0x7362);
+                const uint32_t lo1 = __byte_perm(a[2][q], a[3][q], 0x5140), hi1 = __byte_perm(a[2][q], a[3][q], 0x7362);
+                mma_f16(o[4 * q], pf[s], f16x2_of_codes(uint16_t(lo0 & 0xffffu)), f16x2_of_codes(uint16_t(lo1 & 0xffffu)));
+                mma_f16(o[4 * q + 1], pf[s], f16x2_of_codes(uint16_t(lo0 >> 16)), f16x2_of_codes(uint16_t(lo1 >> 16)));
+                mma_f16(o[4 * q + 2], pf[s], f16x2_of_codes(uint16_t(hi0 & 0xffffu)), f16x2_of_codes(uint16_t(hi1 & 0xffffu)));
+                mma_f16(o[4 * q + 3], pf[s], f16x2_of_codes(uint16_t(hi0 >> 16)), f16x2_of_codes(uint16_t(hi1 >> 16)));
+            }
+        }
+        __syncwarp();
+        const int page2 = page_at(next + kWarps);
+        if (next < iters) load(next, page);
+        cp_async_commit();
+        next += kWarps;
+        page = page2;
+    }
+
+    // ---- merge the warps
+    cp_async_wait<0>();
+    __syncthreads();  // every warp is done with its ring
+    float* om = reinterpret_cast<float*>(smem);
+    float* lm = om + kWarps * kRows * L::OPITCH;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
+        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+        const float inv = l[half] > 0.0f ? ldexpf(1.0f / l[half], vexp - 127 - 14) : 0.0f;
+        float* dst = om + (warp * kRows + g + 8 * half) * L::OPITCH + 2 * c * NT;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            dst[i] = o[i][2 * half] * inv;
+            dst[NT + i] = o[i][2 * half + 1] * inv;
+        }
+        if (c == 0) lm[warp * kRows + g + 8 * half] = l[half] > 0.0f ? m[half] + log2f(l[half]) : -INFINITY;
+    }
+    __syncthreads();
+    constexpr int CPT = kRows * D / kThreads;  // values per thread, all of one row
+    const int i = threadIdx.x / (D / CPT), d0 = (threadIdx.x % (D / CPT)) * CPT;
+    const int r = r0 + i;
+    if (r >= nrows) return;
+    float mx = lm[i];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, lm[w * kRows + i]);
+    const float mz = mx == -INFINITY ? 0.0f : mx;
+    float wt[kWarps], sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += wt[w] = ex2(lm[w * kRows + i] - mz);
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float out_lse = sum > 0.0f ? mx + log2f(sum) : -INFINITY;
+    const int64_t row = int64_t(k.tok0 + r / p.G) * p.Hq + h * p.G + r % p.G;
+    float y[CPT];
+#pragma unroll
+    for (int j = 0; j < CPT; ++j) y[j] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+        for (int j = 0; j < CPT; j += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(om + (w * kRows + i) * L::OPITCH + d0 + j);
+            y[j] = fmaf(wt[w], v.x, y[j]);
+            y[j + 1] = fmaf(wt[w], v.y, y[j + 1]);
+            y[j + 2] = fmaf(wt[w], v.z, y[j + 2]);
+            y[j + 3] = fmaf(wt[w], v.w, y[j + 3]);
+        }
+    if (p.direct) {
+        uint32_t pk[CPT / 2];
+#pragma unroll
+        for (int j = 0; j < CPT; j += 2) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(y[j] * inv, y[j + 1] * inv);
+            pk[j / 2] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(p.O + row * D + d0);
+#pragma unroll
+        for (int j = 0; j < CPT / 8; ++j) dst[j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+        if (d0 == 0 && p.lse) p.lse[row] = out_lse * kLn2;
+    } else {
+        const int64_t at = int64_t(slot) * p.T * p.Hq + row;
+        float4* dst = reinterpret_cast<float4*>(p.part + at * D + d0);
+#pragma unroll
+        for (int j = 0; j < CPT / 4; ++j)
+            dst[j] = make_float4(y[4 * j] * inv, y[4 * j + 1] * inv, y[4 * j + 2] * inv, y[4 * j + 3] * inv);
+        if (d0 == 0) p.part_lse[at] = out_lse;
+    }
+}
+
+// Joins the slots of each row: out = sum_s 2^(lse_s - lse) out_s.  One warp
+// per row; slots whose lse is -inf hold no output and are not read.  Rows
+// outside [q_start[0], q_start[B]) are left as they were.
+template <int D>
+__global__ void __launch_bounds__(256)
+join_kernel(const Params p) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = int64_t(p.T) * p.Hq;
+    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    const int t = int(row / p.Hq);
+    if (t < p.q_start[0] || t >= p.q_start[p.B]) return;
+    const int slots = p.splits_p + p.splits_o;
+    constexpr int VPL = D / 32;  // values per lane
+    float mx = -INFINITY;
+    for (int s = lane; s < slots; s += 32) mx = fmaxf(mx, p.part_lse[int64_t(s) * rows + row]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    const float mz = mx == -INFINITY ? 0.0f : mx;
+    float y[VPL], sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) y[j] = 0.0f;
+    for (int s0 = 0; s0 < slots; s0 += 32) {
+        const int s = s0 + lane;
+        const float w = s < slots ? ex2(p.part_lse[int64_t(s) * rows + row] - mz) : 0.0f;
+        const int n = min(32, slots - s0);
+        for (int i = 0; i < n; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            if (wi > 0.0f) {
+                sum += wi;
+                const float* src = p.part + (int64_t(s0 + i) * rows + row) * D + lane * VPL;
+                if constexpr (VPL == 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(src);
+                    y[0] = fmaf(wi, v.x, y[0]);
+                    y[1] = fmaf(wi, v.y, y[1]);
+                    y[2] = fmaf(wi, v.z, y[2]);
+                    y[3] = fmaf(wi, v.w, y[3]);
+                } else {
+                    const float2 v = *reinterpret_cast<const float2*>(src);
+                    y[0] = fmaf(wi, v.x, y[0]);
+                    y[1] = fmaf(wi, v.y, y[1]);
+                }
+            }
+        }
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + row * D + lane * VPL);
+#pragma unroll
+    for (int j = 0; j < VPL; j += 2) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(y[j] * inv, y[j + 1] * inv);
+        dst[j / 2] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    if (lane == 0 && p.lse) p.lse[row] = sum > 0.0f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+}  // namespace attend
+}  // namespace mfp8

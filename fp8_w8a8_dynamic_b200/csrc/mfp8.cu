@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <map>
@@ -21,6 +22,8 @@
 #include "gemm_cluster.cuh"
 #include "producer.cuh"
 #include "kv8.cuh"
+#include "rope.cuh"
+#include "attend.cuh"
 
 namespace mfp8 {
 namespace {
@@ -814,6 +817,140 @@ struct PickSiluMul {
     static auto kern() { return producer::silu_mul_quant_kernel<producer::kThreads, VPT>; }
 };
 
+// ------------------------------------- rotary positions, paged cache --
+
+// A strided run of T tokens' head rows, in bytes from its start.
+size_t strided_bytes(int64_t T, int64_t ld, int64_t width, size_t elem) {
+    return T == 0 ? 0 : (size_t(T - 1) * size_t(ld) + size_t(width)) * elem;
+}
+
+template <class P>
+bool aligned_to(const P* p) {
+    return (reinterpret_cast<uintptr_t>(p) & (alignof(P) - 1)) == 0;
+}
+
+// page_size -> its log2, or -1.
+int page_shift(int64_t page_size) {
+    for (int s = 3; s <= 8; ++s)
+        if (page_size == int64_t(1) << s) return s;
+    return -1;
+}
+
+bool page_shape_ok(int64_t n_pages, int64_t H, int64_t page_size, int64_t D) {
+    return n_pages >= 0 && n_pages <= INT32_MAX && page_shift(page_size) > 0 &&
+           (n_pages == 0 || H * page_size * D <= (int64_t(1) << 44) / n_pages);
+}
+
+mfp8_status check_rope_args(const int32_t* pos, int n_axes, const uint8_t* axis, const float* inv_freq, int64_t rot,
+                            int64_t D, int layout, double mscale, int64_t T) {
+    if (n_axes < 1 || n_axes > 4 || (layout != MFP8_ROPE_HALF && layout != MFP8_ROPE_INTERLEAVED) ||
+        !std::isfinite(mscale))
+        return MFP8_ERR_INVALID_ARG;
+    if (D <= 0 || D % 16 != 0 || D > 256 || rot < 0 || rot % 16 != 0 || rot > D) return MFP8_ERR_UNSUPPORTED_SHAPE;
+    if (T > 0 && rot > 0) {
+        if (!pos || !inv_freq || (n_axes > 1 && !axis)) return MFP8_ERR_INVALID_ARG;
+        if (!aligned_to(pos) || !aligned_to(inv_freq)) return MFP8_ERR_MISALIGNED;
+    }
+    return MFP8_OK;
+}
+
+mfp8_status launch_rope(rope::Params p, int layout, cudaStream_t stream) {
+    const int heads = p.nq + p.nk + p.nv;
+    const int lpr = p.vpr <= 2 ? 2 : p.vpr <= 4 ? 4 : p.vpr <= 8 ? 8 : p.vpr <= 16 ? 16 : 32;
+    // Whole tokens per block: enough of them to give every thread kItems
+    // vectors, but no more than leaves four blocks for each SM.
+    const int64_t per_block = int64_t(rope::kThreads) * rope::kItems / (int64_t(heads) * lpr);
+    int64_t tpb = per_block < rope::kMaxTokens ? per_block : rope::kMaxTokens;
+    const int64_t spread = p.T / (148 * 4);
+    if (tpb > spread) tpb = spread;
+    if (tpb < 1) tpb = 1;
+    p.tokens_per_block = int(tpb);
+    const dim3 grid(unsigned((p.T + tpb - 1) / tpb));
+    const int smem = int(tpb) * p.rot * int(sizeof(float));
+    auto run = [&](auto kern) { return launch_pdl(kern, grid, rope::kThreads, stream, smem, p); };
+    const bool il = layout == MFP8_ROPE_INTERLEAVED;
+    switch (lpr) {
+        case 2: return il ? run(rope::rope_store_kernel<2, true>) : run(rope::rope_store_kernel<2, false>);
+        case 4: return il ? run(rope::rope_store_kernel<4, true>) : run(rope::rope_store_kernel<4, false>);
+        case 8: return il ? run(rope::rope_store_kernel<8, true>) : run(rope::rope_store_kernel<8, false>);
+        case 16: return il ? run(rope::rope_store_kernel<16, true>) : run(rope::rope_store_kernel<16, false>);
+        default: return il ? run(rope::rope_store_kernel<32, true>) : run(rope::rope_store_kernel<32, false>);
+    }
+}
+
+// ------------------------------------- attention over a shared prefix --
+
+// How the tokens are cut: slots of partial outputs per row for the prefix
+// and for the own tokens, and the row tiles of each.
+struct AttendPlan {
+    int splits_p = 0, splits_o = 0;
+    int64_t tiles_p = 0, tiles_o = 0;
+    bool direct = false;
+    size_t lse_off = 0, total = 0;
+};
+
+constexpr int kAttendSms = 148;
+constexpr int64_t kAttendMax = int64_t(1) << 20;
+
+// Slots for `units` (row tile, KV head) pairs over `len` tokens: enough blocks
+// for four per SM, none with less than the smallest chunk.
+int attend_splits(int64_t units, int64_t len, int64_t min_chunk, int64_t blocks) {
+    int64_t s = (blocks + units - 1) / units;
+    const int64_t most = (len + min_chunk - 1) / min_chunk;
+    if (s > most) s = most;
+    return int(s < 1 ? 1 : s > 256 ? 256 : s);
+}
+
+bool attend_shape_ok(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_len,
+                     int64_t max_pages, int64_t page_size) {
+    return T >= 0 && T <= kAttendMax && B >= 0 && B <= kAttendMax && max_q >= 1 && max_q <= kAttendMax && Hkv >= 1 &&
+           Hq >= Hkv && Hq <= 65536 && Hq % Hkv == 0 && (D == 64 || D == 128) && page_shift(page_size) > 0 &&
+           prefix_len >= 0 && prefix_len <= attend::kMaxTokens && max_pages >= 0 &&
+           max_pages <= attend::kMaxTokens / page_size && T * Hq <= kMaxDim;
+}
+
+AttendPlan attend_plan(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_len,
+                       int64_t max_pages, int64_t page_size) {
+    AttendPlan a;
+    const int64_t G = Hq / Hkv;
+    if (prefix_len > 0) {
+        a.tiles_p = (T * G + attend::kRows - 1) / attend::kRows;
+        a.splits_p = attend_splits(a.tiles_p * Hkv, prefix_len, attend::kMinChunk, kAttendSms * 4);
+    }
+    if (max_pages > 0 || prefix_len == 0) {
+        a.tiles_o = ((max_q < T ? max_q : T) * G + attend::kRows - 1) / attend::kRows;
+        a.splits_o = attend_splits(a.tiles_o * Hkv * B, max_pages * page_size, attend::kMinChunk, kAttendSms * 4);
+    }
+    const int64_t slots = a.splits_p + a.splits_o;
+    a.direct = slots == 1;
+    if (!a.direct) {
+        a.lse_off = size_t(slots) * size_t(T * Hq) * size_t(D) * 4;
+        a.total = a.lse_off + (size_t(slots) * size_t(T * Hq) * 4 + 255) / 256 * 256;
+    }
+    return a;
+}
+
+template <int D>
+mfp8_status launch_attend(const attend::Params& p, int64_t units, int dev, cudaStream_t stream) {
+    using L = attend::RowsLayout<D>;
+    static bool ready[kMaxDevices] = {};
+    {
+        std::lock_guard<std::mutex> lock(g_mu);
+        if (!ready[dev]) {
+            if (cudaFuncSetAttribute(attend::attend_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     L::SMEM) != cudaSuccess) {
+                cudaGetLastError();
+                return MFP8_ERR_CUDA;
+            }
+            ready[dev] = true;
+        }
+    }
+    mfp8_status st = launch_pdl(attend::attend_rows_kernel<D>, dim3(unsigned(units)), attend::kThreads, stream, L::SMEM, p);
+    if (st != MFP8_OK || p.direct) return st;
+    const int64_t rows = int64_t(p.T) * p.Hq;
+    return launch_pdl(attend::join_kernel<D>, dim3(unsigned((rows + 7) / 8)), 256, stream, 0, p);
+}
+
 // The padded run: scales padded, X quantized (unless FUSED), the kernels on
 // N8 channels into the scratch, then the crop.  Every launch here is a plain
 // stream-ordered launch, so the scratch scales are complete before any
@@ -1193,6 +1330,285 @@ int64_t mfp8_kv8_history_tokens(int64_t T) {
     return T < 128 ? 0 : kv8::kGroup * ((T - 128) / kv8::kGroup);
 }
 
+mfp8_status mfp8_rope_frequencies(int64_t rot, double theta, int scaling, double factor, int64_t trained_len,
+                                  double beta_fast, double beta_slow, float* inv_freq_host, double* mscale_host) {
+    if (rot <= 0 || rot % 16 != 0 || rot > 256) return MFP8_ERR_UNSUPPORTED_SHAPE;
+    if (!inv_freq_host || scaling < MFP8_ROPE_SCALE_NONE || scaling > MFP8_ROPE_SCALE_YARN || !std::isfinite(theta) ||
+        !(theta > 1.0) || (scaling != MFP8_ROPE_SCALE_NONE && (!std::isfinite(factor) || !(factor >= 1.0))))
+        return MFP8_ERR_INVALID_ARG;
+    const bool yarn = scaling == MFP8_ROPE_SCALE_YARN;
+    if (yarn && (trained_len < 1 || !std::isfinite(beta_fast) || !(beta_slow > 0.0) || !(beta_fast > beta_slow)))
+        return MFP8_ERR_INVALID_ARG;
+    const double n = double(rot);
+    if (scaling == MFP8_ROPE_SCALE_NTK) theta *= std::pow(factor, n / (n - 2.0));
+    double low = 0.0, high = 0.0;
+    if (yarn) {
+        // the pair that turns `beta` times within the trained length:
+        // trained_len theta^(-2i/rot) = 2 pi beta
+        auto pair = [&](double beta) {
+            return n * std::log(double(trained_len) / (beta * 6.283185307179586)) / (2.0 * std::log(theta));
+        };
+        low = std::fmax(std::floor(pair(beta_fast)), 0.0);
+        high = std::fmin(std::ceil(pair(beta_slow)), n - 1.0);
+        if (high <= low) high = low + 0.001;  // the ramp has some width
+    }
+    for (int64_t i = 0; i < rot / 2; ++i) {
+        double f = std::pow(theta, -2.0 * double(i) / n);
+        if (scaling == MFP8_ROPE_SCALE_LINEAR) f /= factor;
+        if (yarn) {
+            const double ramp = std::fmin(std::fmax((double(i) - low) / (high - low), 0.0), 1.0);
+            f = f / factor * ramp + f * (1.0 - ramp);
+        }
+        inv_freq_host[i] = float(f);
+    }
+    if (mscale_host) *mscale_host = yarn ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    return MFP8_OK;
+}
+
+mfp8_status mfp8_rope(const void* X_bf16, int64_t ldx, int64_t T, int64_t H, int64_t D, const int32_t* pos, int n_axes,
+                      const uint8_t* axis, const float* inv_freq, int64_t rot, int layout, double mscale, void* Y_bf16,
+                      int64_t ldy, void* stream) {
+    if (T < 0 || H < 0 || D < 0 || ldx < 0 || ldy < 0) return MFP8_ERR_INVALID_ARG;
+    mfp8_status st = check_rope_args(pos, n_axes, axis, inv_freq, rot, D, layout, mscale, T);
+    if (st != MFP8_OK) return st;
+    if (H == 0 || H > 65536 || T > kMaxDim || T * H > kMaxDim) return MFP8_ERR_UNSUPPORTED_SHAPE;
+    if (ldx < H * D || ldy < H * D || ldx % 8 != 0 || ldy % 8 != 0 || ldx > kMaxDim || ldy > kMaxDim)
+        return MFP8_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MFP8_OK;
+    if (!X_bf16 || !Y_bf16) return MFP8_ERR_INVALID_ARG;
+    if (!aligned16(X_bf16) || !aligned16(Y_bf16)) return MFP8_ERR_MISALIGNED;
+    const bool in_place = X_bf16 == Y_bf16 && ldx == ldy;
+    if (!in_place && ranges_overlap(X_bf16, strided_bytes(T, ldx, H * D, 2), Y_bf16, strided_bytes(T, ldy, H * D, 2)))
+        return MFP8_ERR_INVALID_ARG;
+    int dev;
+    DeviceInfo info;
+    if ((st = current_device(&dev, &info)) != MFP8_OK) return st;
+    rope::Params p = {};
+    p.X = static_cast<const uint4*>(X_bf16);
+    p.ldx = ldx / 8;
+    p.pos = pos;
+    p.axis = n_axes > 1 ? axis : nullptr;
+    p.inv_freq = inv_freq;
+    p.n_axes = n_axes;
+    p.rot = int(rot);
+    p.mscale = mscale;
+    p.T = int(T);
+    p.nq = int(H);
+    p.vpr = int(D / 8);
+    p.Y = static_cast<uint4*>(Y_bf16);
+    p.ldy = ldy / 8;
+    return launch_rope(p, layout, static_cast<cudaStream_t>(stream));
+}
+
+mfp8_status mfp8_kv_page_store(const void* KV_bf16, int64_t ldkv, const int64_t* slot, int64_t T, int64_t H, int64_t D,
+                               void* pages, float* scale, int64_t n_pages, int64_t page_size, void* stream) {
+    if (T < 0 || H < 0 || D < 0 || ldkv < 0 || n_pages < 0) return MFP8_ERR_INVALID_ARG;
+    if (H == 0 || H > 65536 || D == 0 || D % 16 != 0 || D > 256 || T > kMaxDim || T * H > kMaxDim || ldkv < H * D ||
+        ldkv % 8 != 0 || ldkv > kMaxDim || !page_shape_ok(n_pages, H, page_size, D))
+        return MFP8_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MFP8_OK;
+    if (!KV_bf16 || !slot || (n_pages > 0 && (!pages || !scale))) return MFP8_ERR_INVALID_ARG;
+    if (!aligned16(KV_bf16) || !aligned16(pages) || !aligned16(scale) || !aligned_to(slot)) return MFP8_ERR_MISALIGNED;
+    const size_t in = strided_bytes(T, ldkv, H * D, 2), rows = size_t(n_pages) * size_t(H * page_size);
+    if (ranges_overlap(KV_bf16, in, pages, rows * size_t(D)) || ranges_overlap(KV_bf16, in, scale, rows * 4) ||
+        ranges_overlap(pages, rows * size_t(D), scale, rows * 4) ||
+        ranges_overlap(slot, size_t(T) * 8, pages, rows * size_t(D)) || ranges_overlap(slot, size_t(T) * 8, scale, rows * 4))
+        return MFP8_ERR_INVALID_ARG;
+    int dev;
+    DeviceInfo info;
+    mfp8_status st = current_device(&dev, &info);
+    if (st != MFP8_OK) return st;
+    rope::Params p = {};
+    p.X = static_cast<const uint4*>(KV_bf16);
+    p.ldx = ldkv / 8;
+    p.n_axes = 1;
+    p.T = int(T);
+    p.nv = int(H);
+    p.vpr = int(D / 8);
+    p.slot = slot;
+    p.n_slots = n_pages * page_size;
+    p.ps_shift = page_shift(page_size);
+    p.V = static_cast<uint2*>(pages);
+    p.v_scale = scale;
+    return launch_rope(p, MFP8_ROPE_HALF, static_cast<cudaStream_t>(stream));
+}
+
+mfp8_status mfp8_kv_page_read(const void* pages, const float* scale, int64_t n_pages, int64_t page_size,
+                              const int64_t* slot, int64_t T, int64_t H, int64_t D, void* out_bf16, void* stream) {
+    if (T < 0 || H < 0 || D < 0 || n_pages < 0) return MFP8_ERR_INVALID_ARG;
+    if (H == 0 || H > 65536 || D == 0 || D % 16 != 0 || D > 256 || T > kMaxDim || T * H > kMaxDim ||
+        !page_shape_ok(n_pages, H, page_size, D))
+        return MFP8_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MFP8_OK;
+    if (!out_bf16 || !slot || (n_pages > 0 && (!pages || !scale))) return MFP8_ERR_INVALID_ARG;
+    if (!aligned16(out_bf16) || !aligned16(pages) || !aligned16(scale) || !aligned_to(slot)) return MFP8_ERR_MISALIGNED;
+    const size_t nout = size_t(T * H * D) * 2, rows = size_t(n_pages) * size_t(H * page_size);
+    if (ranges_overlap(out_bf16, nout, pages, rows * size_t(D)) || ranges_overlap(out_bf16, nout, scale, rows * 4) ||
+        ranges_overlap(out_bf16, nout, slot, size_t(T) * 8))
+        return MFP8_ERR_INVALID_ARG;
+    int dev;
+    DeviceInfo info;
+    mfp8_status st = current_device(&dev, &info);
+    if (st != MFP8_OK) return st;
+    const int vpr = int(D / 8);
+    const int lpr = vpr <= 2 ? 2 : vpr <= 4 ? 4 : vpr <= 8 ? 8 : vpr <= 16 ? 16 : 32;
+    const int64_t R = T * H, per_block = int64_t(rope::kThreads / lpr) * rope::kReadItems;
+    const dim3 grid(unsigned((R + per_block - 1) / per_block));
+    auto run = [&](auto kern) {
+        return launch_pdl(kern, grid, rope::kThreads, static_cast<cudaStream_t>(stream), 0,
+                          static_cast<const uint2*>(pages), scale, slot, n_pages * page_size, page_shift(page_size),
+                          int(R), int(H), vpr, static_cast<uint4*>(out_bf16));
+    };
+    switch (lpr) {
+        case 2: return run(rope::page_read_kernel<2>);
+        case 4: return run(rope::page_read_kernel<4>);
+        case 8: return run(rope::page_read_kernel<8>);
+        case 16: return run(rope::page_read_kernel<16>);
+        default: return run(rope::page_read_kernel<32>);
+    }
+}
+
+mfp8_status mfp8_rope_kv_store(const void* QKV_bf16, int64_t ldqkv, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                               const int32_t* pos, int n_axes, const uint8_t* axis, const float* inv_freq, int64_t rot,
+                               int layout, double mscale, const int64_t* slot, void* Q_bf16, void* k_pages,
+                               float* k_scale, void* v_pages, float* v_scale, int64_t n_pages, int64_t page_size,
+                               void* stream) {
+    if (T < 0 || Hq < 0 || Hkv < 0 || D < 0 || ldqkv < 0 || n_pages < 0) return MFP8_ERR_INVALID_ARG;
+    mfp8_status st = check_rope_args(pos, n_axes, axis, inv_freq, rot, D, layout, mscale, T);
+    if (st != MFP8_OK) return st;
+    if (Hq > 65536 || Hkv > 65536) return MFP8_ERR_UNSUPPORTED_SHAPE;
+    const int64_t H = Hq + 2 * Hkv;
+    if (Hq == 0 || Hkv == 0 || T > kMaxDim || T * H > kMaxDim || ldqkv < H * D || ldqkv % 8 != 0 || ldqkv > kMaxDim ||
+        !page_shape_ok(n_pages, Hkv, page_size, D))
+        return MFP8_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MFP8_OK;
+    if (!QKV_bf16 || !Q_bf16 || !slot || (n_pages > 0 && (!k_pages || !k_scale || !v_pages || !v_scale)))
+        return MFP8_ERR_INVALID_ARG;
+    if (!aligned16(QKV_bf16) || !aligned16(Q_bf16) || !aligned16(k_pages) || !aligned16(k_scale) ||
+        !aligned16(v_pages) || !aligned16(v_scale) || !aligned_to(slot))
+        return MFP8_ERR_MISALIGNED;
+    const size_t in = strided_bytes(T, ldqkv, H * D, 2), rows = size_t(n_pages) * size_t(Hkv * page_size);
+    const void* const buf[7] = {QKV_bf16, slot, Q_bf16, k_pages, k_scale, v_pages, v_scale};
+    const size_t len[7] = {in, size_t(T) * 8, size_t(T * Hq * D) * 2, rows * size_t(D), rows * 4, rows * size_t(D), rows * 4};
+    for (int i = 0; i < 7; ++i)
+        for (int j = i + 1 > 2 ? i + 1 : 2; j < 7; ++j)
+            if (ranges_overlap(buf[i], len[i], buf[j], len[j])) return MFP8_ERR_INVALID_ARG;
+    int dev;
+    DeviceInfo info;
+    if ((st = current_device(&dev, &info)) != MFP8_OK) return st;
+    rope::Params p = {};
+    p.X = static_cast<const uint4*>(QKV_bf16);
+    p.ldx = ldqkv / 8;
+    p.pos = pos;
+    p.axis = n_axes > 1 ? axis : nullptr;
+    p.inv_freq = inv_freq;
+    p.n_axes = n_axes;
+    p.rot = int(rot);
+    p.mscale = mscale;
+    p.T = int(T);
+    p.nq = int(Hq);
+    p.nk = p.nv = int(Hkv);
+    p.vpr = int(D / 8);
+    p.Y = static_cast<uint4*>(Q_bf16);
+    p.ldy = Hq * D / 8;
+    p.slot = slot;
+    p.n_slots = n_pages * page_size;
+    p.ps_shift = page_shift(page_size);
+    p.K = static_cast<uint2*>(k_pages);
+    p.k_scale = k_scale;
+    p.V = static_cast<uint2*>(v_pages);
+    p.v_scale = v_scale;
+    return launch_rope(p, layout, static_cast<cudaStream_t>(stream));
+}
+
+size_t mfp8_prefix_attention_workspace_bytes(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D,
+                                             int64_t prefix_len, int64_t max_pages, int64_t page_size) {
+    if (!attend_shape_ok(T, B, max_q, Hq, Hkv, D, prefix_len, max_pages, page_size) || T == 0 || B == 0) return 0;
+    return attend_plan(T, B, max_q, Hq, Hkv, D, prefix_len, max_pages, page_size).total;
+}
+
+mfp8_status mfp8_prefix_attention(const void* Q_bf16, int64_t ldq, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                  const int32_t* q_start, const int32_t* kv_len, int64_t B, int64_t max_q,
+                                  const void* k_pages, const float* k_scale, const void* v_pages, const float* v_scale,
+                                  int64_t n_pages, int64_t page_size, const int32_t* prefix_pages, int64_t prefix_len,
+                                  const int32_t* page_table, int64_t ld_table, int64_t max_pages, float softmax_scale,
+                                  void* O_bf16, float* lse, void* workspace, size_t workspace_bytes_given,
+                                  void* stream) {
+    if (T < 0 || B < 0 || Hq < 0 || Hkv < 0 || D < 0 || ldq < 0 || max_q < 0 || n_pages < 0 || prefix_len < 0 ||
+        max_pages < 0 || ld_table < 0 || !std::isfinite(softmax_scale) || !(softmax_scale > 0.0f))
+        return MFP8_ERR_INVALID_ARG;
+    if (!attend_shape_ok(T, B, max_q, Hq, Hkv, D, prefix_len, max_pages, page_size) ||
+        !page_shape_ok(n_pages, Hkv, page_size, D) || ldq < Hq * D || ldq % 8 != 0 || ldq > kMaxDim ||
+        ld_table < max_pages || ld_table > kMaxDim)
+        return MFP8_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0 || B == 0) return MFP8_OK;
+    const bool cached = prefix_len > 0 || max_pages > 0;
+    if (!Q_bf16 || !O_bf16 || !q_start || !kv_len || (prefix_len > 0 && !prefix_pages) ||
+        (max_pages > 0 && !page_table) ||
+        (cached && (n_pages == 0 || !k_pages || !k_scale || !v_pages || !v_scale)))
+        return MFP8_ERR_INVALID_ARG;
+    if (!aligned16(Q_bf16) || !aligned16(O_bf16) || !aligned16(k_pages) || !aligned16(k_scale) || !aligned16(v_pages) ||
+        !aligned16(v_scale) || !aligned_to(q_start) || !aligned_to(kv_len) || !aligned_to(prefix_pages) ||
+        !aligned_to(page_table) || !aligned_to(lse))
+        return MFP8_ERR_MISALIGNED;
+    const AttendPlan plan = attend_plan(T, B, max_q, Hq, Hkv, D, prefix_len, max_pages, page_size);
+    const size_t rows = size_t(n_pages) * size_t(Hkv * page_size);
+    // inputs, then what is written
+    const void* const buf[12] = {Q_bf16, k_pages, k_scale, v_pages, v_scale, q_start, kv_len, page_table, prefix_pages,
+                                 O_bf16, lse, workspace};
+    const size_t len[12] = {strided_bytes(T, ldq, Hq * D, 2), rows * size_t(D), rows * 4, rows * size_t(D), rows * 4,
+                            size_t(B + 1) * 4, size_t(B) * 4, strided_bytes(B, ld_table, max_pages, 4),
+                            size_t((prefix_len + page_size - 1) / page_size) * 4,
+                            size_t(T * Hq * D) * 2, lse ? size_t(T * Hq) * 4 : 0, plan.total};
+    if (plan.total > 0) {
+        if (!workspace || workspace_bytes_given < plan.total) return MFP8_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return MFP8_ERR_MISALIGNED;
+    }
+    for (int j = 9; j < 12; ++j)
+        for (int i = 0; i < j; ++i)
+            if (len[i] && len[j] && ranges_overlap(buf[i], len[i], buf[j], len[j])) return MFP8_ERR_INVALID_ARG;
+    const int64_t np = plan.tiles_p * plan.splits_p * Hkv, no = plan.tiles_o * plan.splits_o * Hkv * B;
+    if (np + no > INT32_MAX) return MFP8_ERR_UNSUPPORTED_SHAPE;
+    int dev;
+    DeviceInfo info;
+    mfp8_status st = current_device(&dev, &info);
+    if (st != MFP8_OK) return st;
+    attend::Params p = {};
+    p.Q = static_cast<const __nv_bfloat16*>(Q_bf16);
+    p.ldq = ldq;
+    p.q_start = q_start;
+    p.B = int(B);
+    p.T = int(T);
+    p.Hq = int(Hq);
+    p.Hkv = int(Hkv);
+    p.G = int(Hq / Hkv);
+    p.K = static_cast<const uint8_t*>(k_pages);
+    p.k_scale = k_scale;
+    p.V = static_cast<const uint8_t*>(v_pages);
+    p.v_scale = v_scale;
+    p.n_pages = n_pages;
+    p.ps_shift = page_shift(page_size);
+    p.prefix_pages = prefix_pages;
+    p.prefix_len = int(prefix_len);
+    p.table = page_table;
+    p.ld_table = ld_table;
+    p.max_pages = int(max_pages);
+    p.kv_len = kv_len;
+    p.scale_log2 = softmax_scale * 1.4426950408889634f;
+    p.O = static_cast<__nv_bfloat16*>(O_bf16);
+    p.lse = lse;
+    p.part = static_cast<float*>(workspace);
+    p.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.lse_off);
+    p.splits_p = plan.splits_p;
+    p.splits_o = plan.splits_o;
+    p.tiles_p = int(plan.tiles_p);
+    p.tiles_o = int(plan.tiles_o);
+    p.max_q = int(max_q);
+    p.direct = plan.direct;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return D == 128 ? launch_attend<128>(p, np + no, dev, s) : launch_attend<64>(p, np + no, dev, s);
+}
+
 mfp8_status mfp8_debug_kv8_code_check(void* out_u64x2, int64_t n_scale_pairs, uint32_t seed, void* stream) {
     if (!out_u64x2 || n_scale_pairs <= 0 || n_scale_pairs > INT32_MAX) return MFP8_ERR_INVALID_ARG;
     if (!aligned16(out_u64x2)) return MFP8_ERR_MISALIGNED;
@@ -1278,6 +1694,7 @@ const char* mfp8_status_string(mfp8_status status) {
         case MFP8_ERR_CUDA: return "CUDA runtime error";
         case MFP8_ERR_TIMEOUT: return "a kernel's bounded wait ran out";
         case MFP8_ERR_DEVICE: return "device is not compute capability 10.0 (B200)";
+        case MFP8_ERR_INDEX: return "a slot, page or length in device memory is out of range";
     }
     return "unknown status";
 }

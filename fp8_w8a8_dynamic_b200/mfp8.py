@@ -20,6 +20,7 @@ ERR_WORKSPACE = 4
 ERR_CUDA = 5
 ERR_TIMEOUT = 6
 ERR_DEVICE = 7
+ERR_INDEX = 8
 
 PATH_AUTO = 0
 PATH_TILED = 1
@@ -28,6 +29,14 @@ PATH_PAIR = 3
 PATH_FUSED = 4
 
 FLAG_STATIC_WEIGHTS = 1
+
+ROPE_HALF = 0
+ROPE_INTERLEAVED = 1
+
+ROPE_SCALE_NONE = 0
+ROPE_SCALE_LINEAR = 1
+ROPE_SCALE_NTK = 2
+ROPE_SCALE_YARN = 3
 
 
 class Mfp8Error(RuntimeError):
@@ -47,6 +56,7 @@ def lib():
                                "(python -m fp8_w8a8_dynamic_b200.build)")
         L = ctypes.CDLL(LIB_PATH)
         P, i64, sz, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+        f32, f64 = ctypes.c_float, ctypes.c_double
         sig = {
             "mfp8_quantize_weight": (i32, [P, i64, i64, P, P, P]),
             "mfp8_quantize_act": (i32, [P, i64, i64, P, P, P]),
@@ -64,6 +74,15 @@ def lib():
             "mfp8_kv8_quantize": (i32, [P, i64, i64, i64, P, P, P, P]),
             "mfp8_kv8_read": (i32, [P, P, P, i64, P, i64, i64, i64, P, P]),
             "mfp8_kv8_history_tokens": (i64, [i64]),
+            "mfp8_rope_frequencies": (i32, [i64, f64, i32, f64, i64, f64, f64, P, P]),
+            "mfp8_rope": (i32, [P, i64, i64, i64, i64, P, i32, P, P, i64, i32, f64, P, i64, P]),
+            "mfp8_kv_page_store": (i32, [P, i64, P, i64, i64, i64, P, P, i64, i64, P]),
+            "mfp8_kv_page_read": (i32, [P, P, i64, i64, P, i64, i64, i64, P, P]),
+            "mfp8_rope_kv_store": (i32, [P, i64, i64, i64, i64, i64, P, i32, P, P, i64, i32, f64, P, P, P, P, P, P,
+                                         i64, i64, P]),
+            "mfp8_prefix_attention_workspace_bytes": (sz, [i64] * 9),
+            "mfp8_prefix_attention": (i32, [P, i64, i64, i64, i64, i64, P, P, i64, i64, P, P, P, P, i64, i64, P, i64,
+                                            P, i64, i64, f32, P, P, P, sz, P]),
             "mfp8_debug_kv8_code_check": (i32, [P, i64, ctypes.c_uint32, P]),
             "mfp8_e4m3_encode_f32": (i32, [P, i64, P, P]),
             "mfp8_debug_quantize_check": (i32, [P, P]),
@@ -155,6 +174,42 @@ def mfp8_kv8_read(KV_u8, kv_scale, kv_zero, Tq, tail_bf16, Tr, H, D, out_bf16, s
 
 def mfp8_kv8_history_tokens(T):
     return lib().mfp8_kv8_history_tokens(T)
+
+
+def mfp8_rope_frequencies(rot, theta, scaling, factor, trained_len, beta_fast, beta_slow, inv_freq_host, mscale_host):
+    return lib().mfp8_rope_frequencies(rot, theta, scaling, factor, trained_len, beta_fast, beta_slow, inv_freq_host,
+                                       mscale_host)
+
+
+def mfp8_rope(X_bf16, ldx, T, H, D, pos, n_axes, axis, inv_freq, rot, layout, mscale, Y_bf16, ldy, stream=0):
+    return lib().mfp8_rope(X_bf16, ldx, T, H, D, pos, n_axes, axis, inv_freq, rot, layout, mscale, Y_bf16, ldy, stream)
+
+
+def mfp8_kv_page_store(KV_bf16, ldkv, slot, T, H, D, pages, scale, n_pages, page_size, stream=0):
+    return lib().mfp8_kv_page_store(KV_bf16, ldkv, slot, T, H, D, pages, scale, n_pages, page_size, stream)
+
+
+def mfp8_kv_page_read(pages, scale, n_pages, page_size, slot, T, H, D, out_bf16, stream=0):
+    return lib().mfp8_kv_page_read(pages, scale, n_pages, page_size, slot, T, H, D, out_bf16, stream)
+
+
+def mfp8_rope_kv_store(QKV_bf16, ldqkv, T, Hq, Hkv, D, pos, n_axes, axis, inv_freq, rot, layout, mscale, slot, Q_bf16,
+                       k_pages, k_scale, v_pages, v_scale, n_pages, page_size, stream=0):
+    return lib().mfp8_rope_kv_store(QKV_bf16, ldqkv, T, Hq, Hkv, D, pos, n_axes, axis, inv_freq, rot, layout, mscale,
+                                    slot, Q_bf16, k_pages, k_scale, v_pages, v_scale, n_pages, page_size, stream)
+
+
+def mfp8_prefix_attention_workspace_bytes(T, B, max_q, Hq, Hkv, D, prefix_len, max_pages, page_size):
+    return lib().mfp8_prefix_attention_workspace_bytes(T, B, max_q, Hq, Hkv, D, prefix_len, max_pages, page_size)
+
+
+def mfp8_prefix_attention(Q_bf16, ldq, T, Hq, Hkv, D, q_start, kv_len, B, max_q, k_pages, k_scale, v_pages, v_scale,
+                          n_pages, page_size, prefix_pages, prefix_len, page_table, ld_table, max_pages,
+                          softmax_scale, O_bf16, lse, workspace, workspace_bytes, stream=0):
+    return lib().mfp8_prefix_attention(Q_bf16, ldq, T, Hq, Hkv, D, q_start, kv_len, B, max_q, k_pages, k_scale,
+                                       v_pages, v_scale, n_pages, page_size, prefix_pages, prefix_len, page_table,
+                                       ld_table, max_pages, softmax_scale, O_bf16, lse, workspace, workspace_bytes,
+                                       stream)
 
 
 def mfp8_debug_kv8_code_check(out, n_scale_pairs, seed, stream=0):
@@ -384,6 +439,225 @@ class Kv8Cache:
     def read(self, out=None):
         tq = self.Tq
         return kv8_read(self.codes[:tq], self.scale[:tq // 64], self.zero[:tq // 64], self.tail, out=out)
+
+
+class _On:
+    """Where a helper's kernels run: on `stream` (or torch's current one) of
+    the current device, which must hold every tensor.  With a stream other
+    than the current one, outputs are allocated on it and inputs are marked
+    as used by it, so torch's allocator does not hand their memory on early."""
+
+    def __init__(self, where, stream, tensors):
+        import torch
+        dev = torch.cuda.current_device()
+        for t in tensors:
+            if t is not None and (not t.is_cuda or t.get_device() != dev):
+                raise ValueError(f"{where}: tensors must be on the current CUDA device ({dev})")
+        cur = torch.cuda.current_stream()
+        self.device = cur.device
+        self.other = None
+        if stream is not None and stream.cuda_stream != cur.cuda_stream:
+            if stream.device_index != dev:
+                raise ValueError(f"{where}: the stream belongs to another device")
+            self.other = stream
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+        self.handle = (stream or cur).cuda_stream
+
+    def empty(self, shape, dtype):
+        import torch
+        if self.other is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.other):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+
+def _need(ok, where, what):
+    if not ok:
+        raise ValueError(f"{where}: {what}")
+
+
+def _rows(where, x, name="x"):
+    """bf16 [T, H, D] with whole head rows one after the other; elements between tokens."""
+    import torch
+    _need(x.dim() == 3 and x.dtype == torch.bfloat16, where, f"{name} must be bf16 [T, H, D]")
+    T, H, D = x.shape
+    _need(T == 0 or ((D < 2 or x.stride(2) == 1) and (H < 2 or x.stride(1) == D)), where,
+          f"the head rows of a token in {name} must be contiguous")
+    return T, H, D, x.stride(0) if T > 1 else H * D
+
+
+def _rope_args(where, T, pos, inv_freq, axis):
+    """(n_axes, rot) of position and frequency tensors that fit."""
+    import torch
+    _need(pos.dtype == torch.int32 and pos.dim() in (1, 2) and pos.shape[-1] == T and pos.is_contiguous(), where,
+          "pos must be contiguous int32 [T] or [axes, T]")
+    _need(inv_freq.dtype == torch.float32 and inv_freq.dim() == 1 and inv_freq.is_contiguous(), where,
+          "inv_freq must be contiguous fp32 [rot / 2]")
+    n_axes = pos.shape[0] if pos.dim() == 2 else 1
+    _need(n_axes == 1 or axis is not None, where, "several position axes need `axis`")
+    _need(axis is None or (axis.dtype == torch.uint8 and axis.shape == inv_freq.shape and axis.is_contiguous()),
+          where, "axis must be contiguous uint8 [rot / 2]")
+    return n_axes, 2 * inv_freq.numel()
+
+
+def _pool(where, pages, scale, H, D):
+    """(n_pages, page_size) of a paged cache tensor and its scales."""
+    import torch
+    _need(pages.dtype == torch.uint8 and pages.dim() == 4 and pages.is_contiguous() and pages.shape[1] == H
+          and pages.shape[3] == D, where, f"pages must be contiguous uint8 [n_pages, {H}, page_size, {D}]")
+    _need(scale.dtype == torch.float32 and scale.shape == pages.shape[:3] and scale.is_contiguous(), where,
+          "scale must be contiguous fp32 [n_pages, H, page_size]")
+    return pages.shape[0], pages.shape[2]
+
+
+def _slots(where, slot, T=None):
+    import torch
+    _need(slot.dtype == torch.int64 and slot.dim() == 1 and slot.is_contiguous() and (T is None or len(slot) == T),
+          where, "slot must be contiguous int64 [T]")
+
+
+def rope_frequencies(rot, theta, scaling=ROPE_SCALE_NONE, factor=1.0, trained_len=0, beta_fast=32.0, beta_slow=1.0,
+                     device="cuda"):
+    """The frequency table of ``rope``: (fp32 [rot / 2] on `device`, mscale)."""
+    import torch
+    host = torch.empty((max(int(rot), 0) // 2,), dtype=torch.float32)
+    mscale = ctypes.c_double(1.0)
+    _check(mfp8_rope_frequencies(rot, theta, scaling, factor, trained_len, beta_fast, beta_slow, host.data_ptr(),
+                                 ctypes.addressof(mscale)), "mfp8_rope_frequencies")
+    return host.to(device), mscale.value
+
+
+def rope(x, pos, inv_freq, axis=None, layout=ROPE_HALF, mscale=1.0, out=None, stream=None):
+    """Rotary positions: x bf16 [T, H, D] (tokens may be strided, as the query
+    columns of a packed projection) -> rotated bf16 [T, H, D].  pos int32 [T]
+    or [axes, T]; inv_freq fp32 [rot / 2]; axis uint8 [rot / 2].  `out` may
+    be x itself."""
+    import torch
+    T, H, D, ldx = _rows("rope", x)
+    n_axes, rot = _rope_args("rope", T, pos, inv_freq, axis)
+    on = _On("rope", stream, (x, pos, inv_freq, axis, out))
+    if out is None:
+        out = on.empty((T, H, D), torch.bfloat16)
+    _need(out.shape == x.shape, "rope", "out must have x's shape")
+    ldy = _rows("rope", out, "out")[3]
+    _check(mfp8_rope(x.data_ptr(), ldx, T, H, D, pos.data_ptr(), n_axes, _ptr(axis), inv_freq.data_ptr(), rot, layout,
+                     mscale, out.data_ptr(), ldy, on.handle), "mfp8_rope")
+    return out
+
+
+def kv_page_store(kv, slot, pages, scale, stream=None):
+    """Quantize kv bf16 [T, H, D] (tokens may be strided) into the slots (int64
+    [T], negative: skipped) of pages uint8 [n_pages, H, page_size, D] and
+    scale fp32 [n_pages, H, page_size]."""
+    T, H, D, ld = _rows("kv_page_store", kv, "kv")
+    n_pages, ps = _pool("kv_page_store", pages, scale, H, D)
+    _slots("kv_page_store", slot, T)
+    on = _On("kv_page_store", stream, (kv, slot, pages, scale))
+    _check(mfp8_kv_page_store(kv.data_ptr(), ld, slot.data_ptr(), T, H, D, pages.data_ptr(), scale.data_ptr(), n_pages,
+                              ps, on.handle), "mfp8_kv_page_store")
+
+
+def kv_page_read(pages, scale, slot, out=None, stream=None):
+    """The rows in slot int64 [T] of a paged cache as bf16 [T, H, D] (zeros for a negative slot)."""
+    import torch
+    _need(pages.dim() == 4, "kv_page_read", "pages must be uint8 [n_pages, H, page_size, D]")
+    H, D = pages.shape[1], pages.shape[3]
+    n_pages, ps = _pool("kv_page_read", pages, scale, H, D)
+    _slots("kv_page_read", slot)
+    T = slot.shape[0]
+    on = _On("kv_page_read", stream, (pages, scale, slot, out))
+    if out is None:
+        out = on.empty((T, H, D), torch.bfloat16)
+    _need(out.dtype == torch.bfloat16 and out.shape == (T, H, D) and out.is_contiguous(), "kv_page_read",
+          "out must be contiguous bf16 [T, H, D]")
+    _check(mfp8_kv_page_read(pages.data_ptr(), scale.data_ptr(), n_pages, ps, slot.data_ptr(), T, H, D, out.data_ptr(),
+                             on.handle), "mfp8_kv_page_read")
+    return out
+
+
+def rope_kv_store(qkv, n_heads, pos, inv_freq, slot, k_pages, k_scale, v_pages, v_scale, axis=None, layout=ROPE_HALF,
+                  mscale=1.0, out=None, stream=None):
+    """What stands between qkv_proj and attention: qkv bf16 [T, (n_heads + 2
+    Hkv) D] (rows may be strided) -> rotated queries bf16 [T, n_heads, D];
+    rotated keys and values are quantized into their slots.  Hkv and D are
+    those of the pages."""
+    import torch
+    w = "rope_kv_store"
+    _need(k_pages.dim() == 4, w, "pages must be uint8 [n_pages, H, page_size, D]")
+    Hkv, D = k_pages.shape[1], k_pages.shape[3]
+    n_pages, ps = _pool(w, k_pages, k_scale, Hkv, D)
+    _need(_pool(w, v_pages, v_scale, Hkv, D) == (n_pages, ps), w, "k_pages and v_pages must have one shape")
+    _need(qkv.dim() == 2 and qkv.dtype == torch.bfloat16 and qkv.shape[1] == (n_heads + 2 * Hkv) * D
+          and (qkv.shape[0] == 0 or qkv.stride(1) == 1), w, "qkv must be bf16 [T, (n_heads + 2 Hkv) D]")
+    T = qkv.shape[0]
+    n_axes, rot = _rope_args(w, T, pos, inv_freq, axis)
+    _slots(w, slot, T)
+    on = _On(w, stream, (qkv, pos, inv_freq, axis, slot, k_pages, k_scale, v_pages, v_scale, out))
+    if out is None:
+        out = on.empty((T, n_heads, D), torch.bfloat16)
+    _need(out.dtype == torch.bfloat16 and out.shape == (T, n_heads, D) and out.is_contiguous(), w,
+          "out must be contiguous bf16 [T, n_heads, D]")
+    _check(mfp8_rope_kv_store(qkv.data_ptr(), qkv.stride(0) if T > 1 else qkv.shape[1], T, n_heads, Hkv, D,
+                              pos.data_ptr(), n_axes, _ptr(axis), inv_freq.data_ptr(), rot, layout, mscale,
+                              slot.data_ptr(), out.data_ptr(), k_pages.data_ptr(), k_scale.data_ptr(),
+                              v_pages.data_ptr(), v_scale.data_ptr(), n_pages, ps, on.handle), "mfp8_rope_kv_store")
+    return out
+
+
+def prefix_attention(q, q_start, kv_len, page_table, prefix_pages, prefix_len, k_pages, k_scale, v_pages, v_scale,
+                     max_q, scale=None, out=None, want_lse=False, workspace=None, stream=None):
+    """Attention of a batch that shares a prefix, over the paged FP8 cache.
+    q bf16 [T, Hq, D] (tokens may be strided); q_start int32 [B + 1]: sequence
+    b has the query tokens q_start[b] .. q_start[b + 1] - 1, at most max_q;
+    kv_len int32 [B]: its own cached tokens, the query tokens the last of them;
+    page_table int32 [B, max_pages] (a row may be strided) or None;
+    prefix_pages int32 [>= ceil(prefix_len / page_size)] or None, prefix_len
+    an int; scale defaults to D ** -0.5.  -> bf16 [T, Hq, D], with want_lse
+    also the natural log-sum-exp fp32 [T, Hq]."""
+    import torch
+    w = "prefix_attention"
+    T, Hq, D, ldq = _rows(w, q, "q")
+    _need(k_pages.dim() == 4, w, "pages must be uint8 [n_pages, H, page_size, D]")
+    Hkv = k_pages.shape[1]
+    n_pages, ps = _pool(w, k_pages, k_scale, Hkv, D)
+    _need(_pool(w, v_pages, v_scale, Hkv, D) == (n_pages, ps), w, "k_pages and v_pages must have one shape")
+    i32 = torch.int32
+    _need(kv_len.dtype == i32 and kv_len.dim() == 1 and kv_len.is_contiguous(), w, "kv_len must be contiguous int32 [B]")
+    B = kv_len.shape[0]
+    _need(q_start.dtype == i32 and q_start.shape == (B + 1,) and q_start.is_contiguous(), w,
+          "q_start must be contiguous int32 [B + 1]")
+    max_pages = ld = 0
+    if page_table is not None:
+        _need(page_table.dtype == i32 and page_table.dim() == 2 and page_table.shape[0] == B, w,
+              "page_table must be int32 [B, max_pages]")
+        max_pages = page_table.shape[1]
+        _need(max_pages < 2 or page_table.stride(1) == 1, w, "the rows of page_table must be contiguous")
+        ld = page_table.stride(0) if B > 1 else max_pages
+    if prefix_len:
+        _need(prefix_pages is not None and prefix_pages.dtype == i32 and prefix_pages.dim() == 1
+              and prefix_pages.is_contiguous() and 0 < prefix_len <= prefix_pages.shape[0] * ps, w,
+              "prefix_pages must be contiguous int32 and cover prefix_len")
+    on = _On(w, stream, (q, q_start, kv_len, page_table, prefix_pages, k_pages, k_scale, v_pages, v_scale, out,
+                         workspace))
+    if out is None:
+        out = on.empty((T, Hq, D), torch.bfloat16)
+    _need(out.dtype == torch.bfloat16 and out.shape == (T, Hq, D) and out.is_contiguous(), w,
+          "out must be contiguous bf16 [T, Hq, D]")
+    lse = on.empty((T, Hq), torch.float32) if want_lse else None
+    if workspace is None:
+        nbytes = mfp8_prefix_attention_workspace_bytes(T, B, max_q, Hq, Hkv, D, prefix_len, max_pages, ps)
+        workspace = on.empty((nbytes,), torch.uint8) if nbytes else None
+    else:
+        _need(workspace.is_contiguous(), w, "workspace must be contiguous")
+    _check(mfp8_prefix_attention(
+        q.data_ptr(), ldq, T, Hq, Hkv, D, q_start.data_ptr(), kv_len.data_ptr(), B, max_q, k_pages.data_ptr(),
+        k_scale.data_ptr(), v_pages.data_ptr(), v_scale.data_ptr(), n_pages, ps, _ptr(prefix_pages), prefix_len,
+        _ptr(page_table) if max_pages else None, ld, max_pages, scale if scale is not None else D ** -0.5,
+        out.data_ptr(), _ptr(lse), _ptr(workspace), workspace.nbytes if workspace is not None else 0, on.handle),
+        "mfp8_prefix_attention")
+    return (out, lse) if want_lse else out
 
 
 def e4m3_encode(values, stream=None):

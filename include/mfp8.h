@@ -27,7 +27,8 @@
  *     (out_features, in_features) layout), Y is [M, N].  BF16 buffers hold
  *     IEEE bfloat16 bit patterns; FP8 buffers hold float8_e4m3fn codes, one
  *     byte each; scales are fp32.
- *   - Every pointer must be 16-byte aligned.  K must be a positive multiple
+ *   - Every pointer must be 16-byte aligned (arrays of positions, slots,
+ *     pages and lengths need only their element's alignment).  K must be a positive multiple
  *     of 16, N >= 1, M >= 0 (M == 0 is a no-op).  When N is not a multiple
  *     of 8 (rows of Y not 16-byte aligned) the Linear runs its kernels on N
  *     rounded up to 8 channels into scratch taken from the workspace (the
@@ -68,7 +69,8 @@ typedef enum {
     MFP8_ERR_WORKSPACE = 4,         /* workspace missing or smaller than mfp8_linear_workspace_bytes */
     MFP8_ERR_CUDA = 5,              /* a CUDA runtime call or launch failed */
     MFP8_ERR_TIMEOUT = 6,           /* a kernel's bounded wait ran out (device status) */
-    MFP8_ERR_DEVICE = 7             /* the current device is not compute capability 10.0 */
+    MFP8_ERR_DEVICE = 7,            /* the current device is not compute capability 10.0 */
+    MFP8_ERR_INDEX = 8              /* a slot, page or length in device memory is out of range (device status) */
 } mfp8_status;
 
 /* Per-channel weight quantization (one-time, offline).
@@ -305,6 +307,152 @@ MFP8_API mfp8_status mfp8_kv8_read(const void* KV_u8, const float* kv_scale, con
  * positions move into the history. */
 MFP8_API int64_t mfp8_kv8_history_tokens(int64_t T);
 
+/* ------------------------------- rotary positions and the paged KV cache -- */
+
+/* How the values of a head row pair up for the rotation: pair i of rot / 2 is
+ * (x[i], x[i + rot/2]) in the half layout, (x[2i], x[2i+1]) in the
+ * interleaved one. */
+typedef enum { MFP8_ROPE_HALF = 0, MFP8_ROPE_INTERLEAVED = 1 } mfp8_rope_layout;
+
+/* How mfp8_rope_frequencies stretches the frequencies for contexts `factor`
+ * times as long as the model was trained on. */
+typedef enum {
+    MFP8_ROPE_SCALE_NONE = 0,
+    MFP8_ROPE_SCALE_LINEAR = 1, /* every frequency divided by factor (positions interpolated) */
+    MFP8_ROPE_SCALE_NTK = 2,    /* theta raised to theta * factor^(rot / (rot - 2)): the slowest pair is divided by
+                                   factor, the fastest unchanged */
+    MFP8_ROPE_SCALE_YARN = 3    /* "YaRN: Efficient Context Window Extension of Large Language Models" (Peng et al.):
+                                   a pair that turns more than beta_fast times within the trained length keeps its
+                                   frequency, one that turns less than beta_slow times is divided by factor, a linear
+                                   ramp over the pairs between; rows grow by mscale = 0.1 ln(factor) + 1 */
+} mfp8_rope_scaling;
+
+/* Host only: the frequency table of mfp8_rope and its mscale.
+ *   inv_freq_host [rot / 2] fp32, written: theta^(-2i / rot), scaled.
+ *   mscale_host: one double, written (1 unless YARN); may be NULL.
+ * theta > 1, factor >= 1; YARN: trained_len >= 1, beta_fast > beta_slow > 0
+ * (the others ignore these).  Table entries are computed in 64 bits and
+ * rounded once.  Errors: MFP8_ERR_INVALID_ARG (NULL table, unknown scaling, a
+ * parameter out of range), MFP8_ERR_UNSUPPORTED_SHAPE (rot not a positive
+ * multiple of 16 up to 256). */
+MFP8_API mfp8_status mfp8_rope_frequencies(int64_t rot, double theta, int scaling, double factor, int64_t trained_len,
+                                           double beta_fast, double beta_slow, float* inv_freq_host,
+                                           double* mscale_host);
+
+/* Rotary positions ("MOSS-VL-Instruct-0708-FP8 architecture" article:
+ * interleaved M-RoPE, theta 5e6, contexts of 256K positions).  In the first
+ * `rot` values of every head row, with a = pos * inv_freq[i] formed in 64
+ * bits, c = fl32(mscale cos a), s = fl32(mscale sin a):
+ *   y1 = bf16(fl32(fl32(x1 c) - fl32(x2 s))),
+ *   y2 = bf16(fl32(fl32(x2 c) + fl32(x1 s)));
+ * the other D - rot values are copied.
+ *   X_bf16 [T] tokens ldx elements apart, each H rows of D; Y_bf16 the same
+ *       with ldy.  Y may be X (with ldy == ldx); otherwise their ranges must
+ *       not overlap.
+ *   pos [n_axes][T] int32, n_axes in 1 .. 4; a negative position rotates
+ *       back.  axis [rot / 2] u8 names the position axis that each pair
+ *       follows (entries at or above n_axes count as n_axes - 1); NULL with
+ *       n_axes = 1.
+ *   inv_freq [rot / 2] fp32 (device), as from mfp8_rope_frequencies; mscale
+ *       finite.
+ * D a multiple of 16 up to 256, rot a multiple of 16 in 0 .. D (0 copies),
+ * ldx and ldy multiples of 8 and at least H * D.  T == 0 is a no-op. */
+MFP8_API mfp8_status mfp8_rope(const void* X_bf16, int64_t ldx, int64_t T, int64_t H, int64_t D, const int32_t* pos,
+                               int n_axes, const uint8_t* axis, const float* inv_freq, int64_t rot, int layout,
+                               double mscale, void* Y_bf16, int64_t ldy, void* stream);
+
+/* The paged FP8 KV cache: one K or V tensor of a layer is
+ *   pages  [n_pages][H][page_size][D] e4m3 codes, and
+ *   scale  [n_pages][H][page_size] fp32,
+ * page_size a power of two in 8 .. 256.  A token's slot is
+ * page * page_size + place.  Rows are quantized by the rule of
+ * mfp8_kv_quantize, so the bytes are the same.
+ *
+ * Store: row t of KV_bf16 (T tokens ldkv elements apart, each H rows of D)
+ * goes to slot[t] (int64).  A negative slot is padding and is skipped; one at
+ * or above n_pages * page_size is skipped too and recorded as MFP8_ERR_INDEX
+ * in the device status.  Slots of one call must differ: of a slot that
+ * appears twice the contents are unspecified.  Everything else in the pages
+ * stays as it was.  D a multiple of 16 up to 256, ldkv a multiple of 8 and at
+ * least H * D. */
+MFP8_API mfp8_status mfp8_kv_page_store(const void* KV_bf16, int64_t ldkv, const int64_t* slot, int64_t T, int64_t H,
+                                        int64_t D, void* pages, float* scale, int64_t n_pages, int64_t page_size,
+                                        void* stream);
+
+/* Read back: out_bf16 [T][H][D] = bf16(fl32(dec(code) * scale)) of the rows in
+ * slot[t], as mfp8_kv_dequantize; zeros for a negative slot, and for one out
+ * of range, which is recorded as MFP8_ERR_INDEX.  A slot may appear often. */
+MFP8_API mfp8_status mfp8_kv_page_read(const void* pages, const float* scale, int64_t n_pages, int64_t page_size,
+                                       const int64_t* slot, int64_t T, int64_t H, int64_t D, void* out_bf16,
+                                       void* stream);
+
+/* What stands between qkv_proj and attention, in one pass over its packed
+ * output: QKV_bf16 holds T tokens ldqkv elements apart, each Hq query, Hkv
+ * key and Hkv value rows of D.  Queries are rotated into Q_bf16 [T][Hq][D];
+ * keys are rotated, rounded to bf16 and stored, values stored, into slot[t]
+ * of their pages.  The same bytes as mfp8_rope and two mfp8_kv_page_store.
+ * Q_bf16 must not overlap QKV_bf16; arguments and slots as there. */
+MFP8_API mfp8_status mfp8_rope_kv_store(const void* QKV_bf16, int64_t ldqkv, int64_t T, int64_t Hq, int64_t Hkv,
+                                        int64_t D, const int32_t* pos, int n_axes, const uint8_t* axis,
+                                        const float* inv_freq, int64_t rot, int layout, double mscale,
+                                        const int64_t* slot, void* Q_bf16, void* k_pages, float* k_scale,
+                                        void* v_pages, float* v_scale, int64_t n_pages, int64_t page_size,
+                                        void* stream);
+
+/* ------------------------------------- attention over a shared prefix -- */
+
+/* Workspace bytes that are enough for mfp8_prefix_attention at these sizes
+ * (0 for invalid ones): the fp32 partial outputs of the chunks that the
+ * tokens are cut into. */
+MFP8_API size_t mfp8_prefix_attention_workspace_bytes(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv,
+                                                      int64_t D, int64_t prefix_len, int64_t max_pages,
+                                                      int64_t page_size);
+
+/* Attention of B sequences that share a prefix, over the paged FP8 cache.
+ * Sequence b has the query tokens q_start[b] .. q_start[b+1]-1 (one in a
+ * decode step), n_b of them, and kv_len[b] cached tokens of its own behind
+ * the prefix, of which its n_b query tokens are the last.  Query token j of n_b sees the
+ * prefix_len prefix tokens and its own tokens below kv_len[b] - n_b + j + 1.
+ * With G = Hq / Hkv, row (t, h) reads KV head h / G:
+ *   z = softmax_scale * (q . K) over the tokens it sees,
+ *   out = sum e^(z - lse) V,  lse = ln sum e^z;  K, V = dec(code) * scale.
+ * A row that sees nothing gets zeros and lse = -inf.
+ *   Q_bf16: T tokens ldq elements apart, each Hq rows of D.
+ *   q_start [B + 1] int32, not decreasing, within 0 .. T; kv_len [B] int32.
+ *       Tokens outside q_start[0] .. q_start[B] - 1 are left as they were in
+ *       O_bf16 and lse.
+ *   max_q: no sequence has more query tokens (max_q >= 1).
+ *   k_pages, k_scale, v_pages, v_scale: as mfp8_kv_page_store writes them.
+ *   prefix_pages [ceil(prefix_len / page_size)] int32: the prefix's pages in
+ *       order (NULL when prefix_len is 0).
+ *   page_table: B rows ld_table apart of max_pages int32: each sequence's
+ *       own pages in order; entries past its last token are not read.  NULL
+ *       when max_pages is 0.  kv_len[b] is at most max_pages * page_size.
+ *       The work is cut by max_pages, so a table as narrow as the longest
+ *       sequence is the fastest.
+ *   softmax_scale finite and > 0.
+ *   O_bf16 [T][Hq][D]; lse [T][Hq] fp32 or NULL (written).  Neither may
+ *       overlap an input.
+ *   workspace: mfp8_prefix_attention_workspace_bytes(...) bytes, any
+ *       contents; calls that may run at the same time need separate ones.
+ * Lengths, pages and starts are read on the device, so a captured graph may
+ * be replayed with new ones.  Values out of range are cut to what is in range
+ * (a bad page reads page 0), and recorded as MFP8_ERR_INDEX in the device
+ * status.  Sums, softmax statistics and partial outputs are fp32; the
+ * probabilities times the value scales are rounded to 11 bits (f16 relative
+ * to the largest value scale read, so value scales within one call should
+ * lie within 2^28 of one another), the outputs once to bf16.
+ * D is 64 or 128; Hq a multiple of Hkv; B, max_q and T up to 2^20, prefix_len
+ * and max_pages * page_size up to 2^30.  T == 0 or B == 0 is a no-op. */
+MFP8_API mfp8_status mfp8_prefix_attention(const void* Q_bf16, int64_t ldq, int64_t T, int64_t Hq, int64_t Hkv,
+                                           int64_t D, const int32_t* q_start, const int32_t* kv_len, int64_t B,
+                                           int64_t max_q, const void* k_pages, const float* k_scale,
+                                           const void* v_pages, const float* v_scale, int64_t n_pages,
+                                           int64_t page_size, const int32_t* prefix_pages, int64_t prefix_len,
+                                           const int32_t* page_table, int64_t ld_table, int64_t max_pages,
+                                           float softmax_scale, void* O_bf16, float* lse, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
 /* Diagnostic: checks the quantizer's divide-free arithmetic against IEEE
  * divides.  The scale fl32(absmax / 448) of every absmax (0 and each positive
  * finite bf16) is computed as a corrected quotient by 7 times 2^-6, and each
@@ -342,7 +490,7 @@ MFP8_API mfp8_status mfp8_e4m3_encode_f32(const float* in, int64_t n, uint8_t* o
 MFP8_API mfp8_status mfp8_debug_bounded_wait(int64_t timeout_us, void* stream);
 
 /* Synchronises `stream`, then reads and clears the current device's status
- * word.  Returns MFP8_OK, MFP8_ERR_TIMEOUT, or MFP8_ERR_CUDA if the
+ * word.  Returns MFP8_OK, MFP8_ERR_TIMEOUT, MFP8_ERR_INDEX, or MFP8_ERR_CUDA if the
  * synchronisation itself failed. */
 MFP8_API mfp8_status mfp8_get_device_status(void* stream);
 
