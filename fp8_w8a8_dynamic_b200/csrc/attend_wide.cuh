@@ -1,0 +1,604 @@
+// attend_wide.cuh — the tall case of attend.cuh on the tcgen05 tensor cores:
+// many query rows per KV head (a prefix shared by a batch, long prompts), so
+// the work is bound by the products and exponentials instead of by reading
+// the cache.
+//
+// One CTA takes up to 256 query rows of one KV head over one chunk of
+// tokens, 128 tokens to a tile, in two sides of 128 rows whose softmax
+// alternates with the other side's products.  With more than 128 rows the
+// sides hold different rows and share every tile; with fewer they hold the
+// same rows, take alternate tiles and are joined at the end.
+//
+//   z = Q K^T   kind::f8f6f4, M = N = 128.  The key codes go to the tensor
+//               cores as they are.  Q is the sum of two e4m3 terms: bf16 has
+//               8 significant bits, e4m3 has 4, so with q scaled by a power
+//               of two per row, hi = e4m3(q) and lo = e4m3(q - hi) hold q
+//               exactly down to 2^-10 of the row's largest element (which
+//               lies in [224, 448]) and are off by at most 2^-17.8 of it
+//               below.  Two e4m3 products cost what one f16 product costs,
+//               and no key is ever converted.
+//   p           z sk_j (fp32) to e^(z - m), m lagging behind the running
+//               maximum by up to kLag octaves, so O is rescaled only when
+//               the maximum has grown by more.  p sv_j / M 2^kNorm goes to
+//               f16 (M: a power of two above the largest value scale seen).
+//   O += P V    kind::f16, P from TMEM (it replaces z there), V converted
+//               from e4m3 to f16 (exact) by a warpgroup of its own, token
+//               rows of 64 dimensions, read by the MMA with N contiguous.
+//
+// Warps: 0-3 and 4-7 softmax of side 0 and 1 (one row per thread), 8-11 the
+// conversion of V, 12 the TMA loads, one lane per page of the tile, 13 the
+// MMA issue; 14 and 15 only pad the last warpgroup.
+//
+// TMEM: columns 0-127 and 128-255 z (then P) of side 0 and 1, 256 and 384 O.
+// The MMAs of a thread run in order, so Q K^T of a side's next tile may
+// overwrite its P as soon as P V has been issued.
+//
+// Every wait is bounded (mbar_wait), as in the GEMM kernels.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attend.cuh"
+#include "ptx.cuh"
+
+namespace mfp8 {
+namespace attend {
+
+constexpr int kWideThreads = 512;
+constexpr int kTile = 128;      // tokens per tile, rows per side
+constexpr int kWideRows = 256;  // rows per CTA
+constexpr float kLag = 4.0f;
+constexpr int kNorm = 11;  // p < 2^kLag, sv / M <= 1: f16 values below 2^15
+
+template <int D>
+struct WideLayout {
+    static constexpr int KST = 3, VST = 2, CST = 2;
+    static constexpr int Q_OFF = 0;  // [side][hi, lo][128 rows of D bytes]
+    static constexpr int QB = kTile * D;
+    static constexpr int K_OFF = Q_OFF + 4 * QB;
+    static constexpr int V_OFF = K_OFF + KST * kTile * D;
+    static constexpr int C_OFF = V_OFF + VST * kTile * D;       // f16 V: [dim / 64][token][64 dims]
+    static constexpr int VS_OFF = C_OFF + CST * kTile * D * 2;  // scales as loaded: sk, sv
+    static constexpr int CS_OFF = VS_OFF + VST * 1024;          // scales for the softmax: sk, sv (0 past the end)
+    static constexpr int VE_OFF = CS_OFF + CST * 1024;          // largest sv's bits of each converting warp
+    static constexpr int BAR_OFF = VE_OFF + CST * 16;
+    static constexpr int KFULL = 0, KEMPTY = KST, VFULL = 2 * KST, VEMPTY = VFULL + VST, CFULL = VEMPTY + VST,
+                         CEMPTY = CFULL + CST, SFULL = CEMPTY + CST, PFULL = SFULL + 2, OFULL = PFULL + 2,
+                         QFULL = OFULL + 2, DRAIN = QFULL + 1, NUM_BARS = DRAIN + 1;
+    static constexpr int LSE_OFF = BAR_OFF + NUM_BARS * 8;  // [128] log-sum-exps of side 1 at the end
+    static constexpr int MISC_OFF = LSE_OFF + 512;
+    static constexpr int USED = MISC_OFF + 16;
+    static constexpr int SMEM_BYTES = USED + 1024;  // slack for 1024-byte alignment
+    static_assert(BAR_OFF % 8 == 0, "barriers are 8-byte aligned");
+    static_assert(SMEM_BYTES <= 227 * 1024, "one CTA per SM");
+};
+
+// K-major 8-bit operand rows of D bytes, D-byte swizzle (128 or 64).
+template <int D>
+__device__ __forceinline__ uint64_t kmajor_desc(uint32_t addr) {
+    uint64_t d = uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) | (uint64_t((8 * D) >> 4) << 32) |
+                 (uint64_t(1) << 46);
+    return d | (uint64_t(D == 128 ? 2u : 4u) << 61);
+}
+
+// f16 [token][64 dims] blocks of 128-byte rows (128-byte swizzle) as an
+// operand whose N (the dimensions) is contiguous: 8-token groups 1024 bytes
+// apart, 64-dimension blocks kTile * 128 bytes apart.
+__device__ __forceinline__ uint64_t nmajor_desc(uint32_t addr) {
+    return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t((kTile * 128) >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// f16 x f16 -> fp32, A from TMEM, B with N contiguous, shape 128 x N x 16.
+__device__ __forceinline__ constexpr uint32_t idesc_pv(uint32_t N) {
+    return (1u << 4) | (1u << 16) | ((N >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Which part and unit of the grid a CTA works on.
+struct WideGrid {
+    int pairs_p, pairs_o;  // 256-row groups of the prefix's rows, of one sequence's rows
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWideThreads, 1)
+attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV) {
+    using L = WideLayout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    auto bar = [&](int i) { return sb + uint32_t(L::BAR_OFF) + 8u * uint32_t(i); };
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
+    const uint32_t warp = warp_id_sync();
+    const int lane = int(lane_id());
+
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // ---- which rows, which tokens (uniform over the CTA)
+    int64_t u = blockIdx.x;
+    const int64_t np = int64_t(wg.pairs_p) * p.splits_p * p.Hkv;
+    int split, h, pair;
+    Task k;
+    h = int(u % p.Hkv);
+    if (u < np) {
+        u /= p.Hkv;
+        split = int(u % p.splits_p);
+        pair = int(u / p.splits_p);
+        k = prefix_task(p);
+    } else {
+        u = (u - np) / p.Hkv;
+        split = int(u % p.splits_o);
+        u /= p.splits_o;
+        pair = int(u % wg.pairs_o);
+        k = own_task(p, int(u / wg.pairs_o));
+    }
+    const int nrows = k.n * p.G;
+    const int r0 = pair * kWideRows;
+    if (r0 >= nrows) return;
+    const bool both = nrows - r0 > kTile;  // the sides hold different rows
+    const int rlast = min(r0 + kWideRows, nrows) - 1;
+    const int seen = max(visible(k, rlast / p.G), 0);
+    int chunk = (k.len + k.splits - 1) / k.splits;
+    chunk = max((chunk + kTile - 1) / kTile * kTile, kTile);
+    const int64_t first = int64_t(split) * chunk;
+    const int slot = k.slot0 + split;
+    const int64_t all_rows = int64_t(p.T) * p.Hq;
+    auto row_of = [&](int r) { return int64_t(k.tok0 + r / p.G) * p.Hq + h * p.G + r % p.G; };
+    if (first >= seen) {  // nothing here
+        for (int r = r0 + int(threadIdx.x); r <= rlast; r += kWideThreads) {
+            if (!p.direct) p.part_lse[int64_t(slot) * all_rows + row_of(r)] = -INFINITY;
+            else if (p.lse) p.lse[row_of(r)] = -INFINITY;
+        }
+        if (p.direct)
+            for (int i = threadIdx.x; i < (rlast - r0 + 1) * (D / 8); i += kWideThreads)
+                reinterpret_cast<uint4*>(p.O)[row_of(r0 + i / (D / 8)) * (D / 8) + i % (D / 8)] =
+                    make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
+    const int k0 = int(first), k1 = min(k0 + chunk, seen);
+    const int nt = (k1 - k0 + kTile - 1) / kTile;
+    const int steps = both ? 2 * nt : nt;  // step j: side j % 2, tile j / 2 (both) or j
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < L::NUM_BARS; ++i) {
+            uint32_t n = 1;
+            if (i >= L::VEMPTY && i < L::VEMPTY + L::VST) n = 4;  // converting warps
+            if (i >= L::CFULL && i < L::CFULL + L::CST) n = 4;
+            if (i >= L::PFULL && i < L::PFULL + 2) n = 4;  // softmax warps of the side
+            if (i == L::QFULL) n = 8;
+            mbar_init(bar(i), n);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    if (warp == 13) {
+        tmem_alloc(smem_u32(tmem_holder), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+
+    if (warp < 8) {
+        // ------------------------------------------------------ softmax
+        const int side = int(warp >> 2);
+        const int i = int(threadIdx.x & 127);
+        const int r = r0 + (both ? side * kTile : 0) + i;
+        const bool live = r < nrows;
+        const int t = live ? r / p.G : 0;
+        // Q: two e4m3 terms
+        float f;
+        {
+            const uint4* q = reinterpret_cast<const uint4*>(p.Q + int64_t(k.tok0 + t) * p.ldq +
+                                                            int64_t(h * p.G + (live ? r % p.G : 0)) * D);
+            uint32_t acc = 0;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) acc = absmax_bits_u4(live ? q[c] : make_uint4(0u, 0u, 0u, 0u), acc);
+            const uint32_t amax = max(acc & 0xffffu, acc >> 16);
+            // 2^e puts the largest element in [224, 448]: its exponent at 8, or at 7 above 1.75 * 2^n
+            int e = max(int(amax >> 7), 10) - 127 - 8;
+            if ((amax & 0x7fu) > 0x60u) ++e;
+            const float m = pow2i(-e);
+            f = fmaxf(p.scale_log2 * pow2i(e), kFltMin);
+            const uint32_t hi = sb + L::Q_OFF + side * 2 * L::QB + i * D, lo = hi + L::QB;
+            const uint32_t x = D == 128 ? uint32_t(i & 7) : uint32_t((i >> 1) & 3);
+#pragma unroll 2
+            for (int c = 0; c < D / 16; ++c) {
+                const uint4 a = live ? q[2 * c] : make_uint4(0u, 0u, 0u, 0u);
+                const uint4 b = live ? q[2 * c + 1] : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                uint32_t ch[4] = {0u, 0u, 0u, 0u}, cl[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float v0 = bf16_lo(w[j]) * m, v1 = bf16_hi(w[j]) * m;
+                    const uint32_t c2 = e4m3x2(v0, v1);
+                    const uint32_t h2 = f16x2_of_codes(uint16_t(c2));
+                    const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                    ch[j >> 1] |= c2 << (16 * (j & 1));
+                    cl[j >> 1] |= e4m3x2(v0 - back.x, v1 - back.y) << (16 * (j & 1));
+                }
+                const uint32_t at = (uint32_t(c) ^ x) << 4;
+                st_shared_v4(hi + at, ch[0], ch[1], ch[2], ch[3]);
+                st_shared_v4(lo + at, cl[0], cl[1], cl[2], cl[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::QFULL));
+        }
+        const int lim = live ? min(visible(k, t), k1) : 0;
+        const int all_see = k.prefix ? k1 : min(visible(k, (r0 + (both ? side * kTile : 0)) / p.G), k1);
+        const uint32_t lane_base = tmem + ((warp & 3u) << 21);
+        const uint32_t tS = lane_base + uint32_t(side) * 128u, tO = lane_base + 256u + uint32_t(side) * 128u;
+        float m = -INFINITY, l = 0.0f;
+        int vexp = 27, n = 0;
+        const uint64_t f2 = pack2(f, f);
+        for (int j = side; j < steps; j += 2, ++n) {
+            const int tile = both ? j >> 1 : j;
+            const int cs = tile % L::CST;
+            if (!mbar_wait(bar(L::CFULL + cs), (tile / L::CST) & 1, abort_flag)) break;
+            if (!mbar_wait(bar(L::SFULL + side), n & 1, abort_flag)) break;
+            tc_fence_after();
+            const uint32_t sk = sb + L::CS_OFF + cs * 1024;
+            const int base = k0 + tile * kTile;
+            const bool masked = base + kTile > all_see;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t z[32];
+                tmem_ld_32x32b_x32(tS + c * 32, z);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 32; q += 4) {
+                    const float4 s = ld_shared_f4(sk + (c * 32 + q) * 4);
+                    float z0 = __uint_as_float(z[q]) * s.x, z1 = __uint_as_float(z[q + 1]) * s.y;
+                    float z2 = __uint_as_float(z[q + 2]) * s.z, z3 = __uint_as_float(z[q + 3]) * s.w;
+                    if (masked) {
+                        const int tok = base + c * 32 + q;
+                        if (tok >= lim) z0 = -INFINITY;
+                        if (tok + 1 >= lim) z1 = -INFINITY;
+                        if (tok + 2 >= lim) z2 = -INFINITY;
+                        if (tok + 3 >= lim) z3 = -INFINITY;
+                    }
+                    mx = fmaxf(fmaxf(mx, fmaxf(z0, z1)), fmaxf(z2, z3));
+                }
+            }
+            mx *= f;
+            // the largest value scale of the tile, as a power of two above it
+            const uint4 ve4 = lds128(sb + L::VE_OFF + cs * 16);
+            const int ve = max(vexp, min(int(max(max(ve4.x, ve4.y), max(ve4.z, ve4.w)) >> 23) + 1, 254));
+            // m = -inf (nothing seen yet) has -inf + kLag below every finite maximum
+            if (__any_sync(0xffffffffu, mx > m + kLag || ve != vexp)) {
+                const float mn = fmaxf(m, mx);
+                const float keep = mn == -INFINITY ? 1.0f : ex2(m - mn);
+                m = mn;
+                l *= keep;
+                if (n > 0) {
+                    const float scale = keep * pow2i(max(vexp - ve, -126));
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(tO + c * 32, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * scale);
+                        tmem_st_32x32b_x32(tO + c * 32, o);
+                    }
+                }
+                vexp = ve;
+            }
+            const float mz = m == -INFINITY ? 0.0f : m;
+            const uint64_t nm2 = pack2(-mz, -mz);
+            const float vn = pow2i(kNorm - (vexp - 127));
+            const uint64_t vn2 = pack2(vn, vn);
+            uint64_t sum2 = pack2(0.0f, 0.0f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t z[32], w[16];
+                tmem_ld_32x32b_x32(tS + c * 32, z);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 32; q += 4) {
+                    const float4 s = ld_shared_f4(sk + (c * 32 + q) * 4);
+                    const float4 v = ld_shared_f4(sk + 512 + (c * 32 + q) * 4);
+                    float z0, z1, z2, z3;
+                    uint64_t a = mul2(pack2(__uint_as_float(z[q]), __uint_as_float(z[q + 1])), pack2(s.x, s.y));
+                    uint64_t b = mul2(pack2(__uint_as_float(z[q + 2]), __uint_as_float(z[q + 3])), pack2(s.z, s.w));
+                    unpack2(fma2(a, f2, nm2), z0, z1);
+                    unpack2(fma2(b, f2, nm2), z2, z3);
+                    if (masked) {
+                        const int tok = base + c * 32 + q;
+                        if (tok >= lim) z0 = -INFINITY;
+                        if (tok + 1 >= lim) z1 = -INFINITY;
+                        if (tok + 2 >= lim) z2 = -INFINITY;
+                        if (tok + 3 >= lim) z3 = -INFINITY;
+                    }
+                    a = pack2(ex2(z0), ex2(z1));
+                    b = pack2(ex2(z2), ex2(z3));
+                    sum2 = add2(sum2, add2(a, b));
+                    unpack2(mul2(mul2(a, vn2), pack2(v.x, v.y)), z0, z1);
+                    unpack2(mul2(mul2(b, vn2), pack2(v.z, v.w)), z2, z3);
+                    w[q / 2] = pack_f16x2(z0, z1);
+                    w[q / 2 + 1] = pack_f16x2(z2, z3);
+                }
+                tmem_st_32x32b_x16(tS + c * 16, w);  // over columns of z that have been read
+            }
+            float s0, s1;
+            unpack2(sum2, s0, s1);
+            l += s0 + s1;
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::PFULL + side));
+        }
+        // ---- the output of this side's tiles
+        const int mine = both ? nt : (nt + 1 - side) / 2;
+        bool ok = mine > 0 && n == mine && mbar_wait(bar(L::OFULL + side), 0, abort_flag);
+        if (!both && side == 1 && ok) ok = mbar_wait(bar(L::OFULL), 0, abort_flag);  // every MMA is done
+        tc_fence_after();
+        const float inv = ok && l > 0.0f ? ldexpf(1.0f / l, vexp - 127 - kNorm) : 0.0f;
+        float my_lse = ok && l > 0.0f ? m + log2f(l) : -INFINITY;
+        float* buf = reinterpret_cast<float*>(smem + L::Q_OFF);  // [D][128]: side 1's output when joined
+        float* lbuf = reinterpret_cast<float*>(smem + L::LSE_OFF);
+        float w0 = 1.0f, w1 = 0.0f;
+        const bool join = !both && nt > 1;  // uniform
+        if (join) {
+            if (side == 1) {
+                lbuf[i] = my_lse;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(tO + c * 32, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) buf[(c * 32 + q) * 128 + i] = __uint_as_float(o[q]) * inv;
+                }
+            }
+            named_bar_sync(1, 256);
+            const float other = lbuf[i];
+            const float mxl = fmaxf(my_lse, other);
+            if (mxl == -INFINITY) {
+                w0 = 0.0f;
+            } else {
+                w0 = ex2(my_lse - mxl);
+                w1 = ex2(other - mxl);
+                const float tot = w0 + w1;
+                w0 /= tot;
+                w1 /= tot;
+                my_lse = mxl + log2f(tot);
+            }
+        }
+        if (both || side == 0) {  // uniform over the warp, as tcgen05.ld wants
+            // O is finite wherever this side had a tile (its P is 0 for what it does not see)
+            const int64_t row = live ? row_of(r) : 0;
+            const float s = inv * w0;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                float y[32];
+                tmem_ld_32x32b_x32(tO + c * 32, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 32; ++q) {
+                    y[q] = __uint_as_float(o[q]) * s;
+                    if (join) y[q] = fmaf(buf[(c * 32 + q) * 128 + i], w1, y[q]);
+                }
+                if (live && p.direct) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.O + row * D + c * 32);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(y[8 * q + 2 * e], y[8 * q + 2 * e + 1]);
+                            pk[e] = *reinterpret_cast<const uint32_t*>(&b);
+                        }
+                        dst[q] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                } else if (live) {
+                    float4* dst = reinterpret_cast<float4*>(p.part + (int64_t(slot) * all_rows + row) * D + c * 32);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) dst[q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+                }
+            }
+            if (live && !p.direct) p.part_lse[int64_t(slot) * all_rows + row] = my_lse;
+            else if (live && p.lse) p.lse[row] = my_lse == -INFINITY ? -INFINITY : my_lse * kLn2;
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------- V: e4m3 to f16
+        const int tid = int(threadIdx.x) - 256;
+        constexpr int CH = D / 16;        // 16-code pieces per token
+        constexpr int RPI = 128 / CH;     // tokens per pass
+        const int ch = tid % CH;
+        for (int tile = 0; tile < nt; ++tile) {
+            const int vs = tile % L::VST, cs = tile % L::CST;
+            const int valid = min(kTile, k1 - (k0 + tile * kTile));
+            if (!mbar_wait(bar(L::VFULL + vs), (tile / L::VST) & 1, abort_flag)) break;
+            if (!mbar_wait(bar(L::CEMPTY + cs), ((tile / L::CST) & 1) ^ 1, abort_flag)) break;
+            const uint32_t src = sb + L::V_OFF + vs * kTile * D, dst = sb + L::C_OFF + cs * kTile * D * 2;
+            const float skv = ld_shared_f32(sb + L::VS_OFF + vs * 1024 + tid * 4);
+            const float svv = tid < valid ? ld_shared_f32(sb + L::VS_OFF + vs * 1024 + 512 + tid * 4) : 0.0f;
+            float* sc = reinterpret_cast<float*>(smem + L::CS_OFF + cs * 1024);
+            sc[tid] = skv;  // columns past the end are masked by the softmax
+            sc[128 + tid] = svv;
+            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(svv));
+            if (lane == 0) reinterpret_cast<uint32_t*>(smem + L::VE_OFF + cs * 16)[warp - 8] = top;
+#pragma unroll
+            for (int a = 0; a < CH; ++a) {
+                const int row = a * RPI + tid / CH;
+                const uint32_t x = D == 128 ? uint32_t(row & 7) : uint32_t((row >> 1) & 3);
+                uint4 v = lds128(src + row * D + ((uint32_t(ch) ^ x) << 4));
+                if (row >= valid) v = make_uint4(0u, 0u, 0u, 0u);  // whatever the page holds there, NaN codes too
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    o[2 * q] = f16x2_of_codes(uint16_t(w[q] & 0xffffu));
+                    o[2 * q + 1] = f16x2_of_codes(uint16_t(w[q] >> 16));
+                }
+                // 32 bytes: pieces 2 (ch % 4) and + 1 of the row in block ch / 4; the lanes of the other block
+                // write theirs in the other order, so that eight lanes touch eight pieces
+                const uint32_t at = dst + (ch >> 2) * (kTile * 128) + row * 128;
+                const uint32_t flip = uint32_t(ch >> 2) & 1u;
+                const uint32_t p0 = ((uint32_t(ch & 3) * 2u + flip) ^ uint32_t(row & 7)) << 4;
+                const uint32_t p1 = ((uint32_t(ch & 3) * 2u + (flip ^ 1u)) ^ uint32_t(row & 7)) << 4;
+                if (flip) {
+                    st_shared_v4(at + p0, o[4], o[5], o[6], o[7]);
+                    st_shared_v4(at + p1, o[0], o[1], o[2], o[3]);
+                } else {
+                    st_shared_v4(at + p0, o[0], o[1], o[2], o[3]);
+                    st_shared_v4(at + p1, o[4], o[5], o[6], o[7]);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(L::CFULL + cs));
+                mbar_arrive(bar(L::VEMPTY + vs));
+            }
+        }
+    } else if (warp == 12) {
+        // -------------------------------------------------------- loads
+        const int ps = 1 << p.ps_shift;
+        const int box = min(ps, kTile);       // rows of one copy
+        const int per = kTile / box;          // copies of a full tile, one per lane
+        int issued = 0;
+        auto page_for = [&](int tile) {
+            const int tok = k0 + tile * kTile + lane * box;
+            return tile < nt && lane < per && tok < k1 ? page_of(p, k, tok, k1 - 1) : -1;
+        };
+        int page = page_for(0);
+        for (int tile = 0; tile < nt; ++tile) {
+            const int next = page_for(tile + 1);
+            const int ks = tile % L::KST, vs = tile % L::VST;
+            const int base = k0 + tile * kTile;
+            const int copies = min(per, (k1 - base + box - 1) / box);
+            const int32_t row = int32_t(((int64_t(page) * p.Hkv + h) << p.ps_shift) + (base & (ps - 1)));
+            bool ok = mbar_wait(bar(L::KEMPTY + ks), ((tile / L::KST) & 1) ^ 1, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (lane == 0) mbar_arrive_expect_tx(bar(L::KFULL + ks), uint32_t(copies * box * D));
+            __syncwarp();
+            if (lane < copies) tma_load_2d(sb + L::K_OFF + ks * kTile * D + lane * box * D, &tmK, bar(L::KFULL + ks), 0, row);
+            ok = mbar_wait(bar(L::VEMPTY + vs), ((tile / L::VST) & 1) ^ 1, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (lane == 0) mbar_arrive_expect_tx(bar(L::VFULL + vs), uint32_t(copies * box * (D + 8)));
+            __syncwarp();
+            if (lane < copies) {
+                tma_load_2d(sb + L::V_OFF + vs * kTile * D + lane * box * D, &tmV, bar(L::VFULL + vs), 0, row);
+                const uint32_t sc = sb + L::VS_OFF + vs * 1024 + lane * box * 4;
+                bulk_load(sc, p.k_scale + row, uint32_t(box * 4), bar(L::VFULL + vs));
+                bulk_load(sc + 512, p.v_scale + row, uint32_t(box * 4), bar(L::VFULL + vs));
+            }
+            page = next;
+            ++issued;
+        }
+        if (*abort_flag && lane == 0) {
+            // Let every copy still in flight land before the CTA exits.
+            volatile int no_abort = 0;
+            for (int t = max(issued - 3, 0); t <= issued && t < nt; ++t) {
+                mbar_wait(bar(L::KFULL + t % L::KST), (t / L::KST) & 1, &no_abort, 10000000ull);
+                mbar_wait(bar(L::VFULL + t % L::VST), (t / L::VST) & 1, &no_abort, 10000000ull);
+            }
+        }
+    } else if (warp == 13 && lane == 0) {
+        // ---------------------------------------------------------- MMA
+        constexpr uint32_t idesc_s = idesc_e4m3_f32(128, kTile);
+        constexpr uint32_t idesc_o = idesc_pv(D);
+        bool any = false;
+        int done[2] = {0, 0};  // P tiles consumed by each side
+        auto pv = [&](int side, int tile) {
+            if (!mbar_wait(bar(L::PFULL + side), done[side] & 1, abort_flag)) return false;
+            // CFULL needs no wait here: the side's softmax, which PFULL follows, waited for it; but the MMA's
+            // reads are ordered behind the converting warps only through this thread's own wait
+            if (!mbar_wait(bar(L::CFULL + tile % L::CST), (tile / L::CST) & 1, abort_flag)) return false;
+            tc_fence_after();
+            const uint32_t v = sb + L::C_OFF + (tile % L::CST) * kTile * D * 2;
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+                mma_f16_tmem_a(tmem + 256u + uint32_t(side) * 128u, tmem + uint32_t(side) * 128u + kk * 8,
+                               nmajor_desc(v + kk * 2048), idesc_o, (done[side] | kk) != 0);
+            any = true;
+            ++done[side];
+            if (!both || side == 1) mma_commit(bar(L::CEMPTY + tile % L::CST));
+            return true;
+        };
+        bool ok = mbar_wait(bar(L::QFULL), 0, abort_flag);
+        for (int j = 0; j < steps && ok; ++j) {
+            const int side = j & 1, tile = both ? j >> 1 : j;
+            if (j >= 2) ok = pv(side, both ? tile - 1 : tile - 2);
+            if (!ok) break;
+            const int ks = tile % L::KST;
+            ok = mbar_wait(bar(L::KFULL + ks), (tile / L::KST) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t kb = sb + L::K_OFF + ks * kTile * D, qb = sb + L::Q_OFF + side * 2 * L::QB;
+#pragma unroll
+            for (int kk = 0; kk < 2 * (D / 32); ++kk) {
+                const uint32_t term = kk >= D / 32 ? uint32_t(L::QB) : 0u, off = uint32_t(kk % (D / 32)) * 32u;
+                mma_f8(tmem + uint32_t(side) * 128u, kmajor_desc<D>(qb + term + off), kmajor_desc<D>(kb + off), idesc_s,
+                       kk != 0);
+            }
+            any = true;
+            mma_commit(bar(L::SFULL + side));
+            if (!both || side == 1) mma_commit(bar(L::KEMPTY + ks));
+        }
+        for (int j = max(steps, 2); j < steps + 2 && ok; ++j) {  // the last tile of each side
+            const int side = j & 1;
+            ok = pv(side, both ? (j >> 1) - 1 : j - 2);
+            if (ok) mma_commit(bar(L::OFULL + side));
+        }
+        if (*abort_flag && any) {
+            // Wait for the tensor cores to finish before TMEM is freed.
+            volatile int no_abort = 0;
+            mma_commit(bar(L::DRAIN));
+            mbar_wait(bar(L::DRAIN), 0, &no_abort, 10000000ull);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 13) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace attend
+}  // namespace mfp8

@@ -24,6 +24,7 @@
 #include "kv8.cuh"
 #include "rope.cuh"
 #include "attend.cuh"
+#include "attend_wide.cuh"
 
 namespace mfp8 {
 namespace {
@@ -880,9 +881,11 @@ mfp8_status launch_rope(rope::Params p, int layout, cudaStream_t stream) {
 
 // ------------------------------------- attention over a shared prefix --
 
-// How the tokens are cut: slots of partial outputs per row for the prefix
-// and for the own tokens, and the row tiles of each.
+// How the work is cut: which kernel takes the prefix and the own tokens, the
+// slots of partial outputs per row of each, and their row tiles (of 16 rows,
+// or of 256 for the tall kernel).
 struct AttendPlan {
+    bool wide_p = false, wide_o = false;
     int splits_p = 0, splits_o = 0;
     int64_t tiles_p = 0, tiles_o = 0;
     bool direct = false;
@@ -891,14 +894,30 @@ struct AttendPlan {
 
 constexpr int kAttendSms = 148;
 constexpr int64_t kAttendMax = int64_t(1) << 20;
+constexpr int64_t kWideFrom = 17;  // query rows per KV head from which the tall kernel takes a part
 
-// Slots for `units` (row tile, KV head) pairs over `len` tokens: enough blocks
-// for four per SM, none with less than the smallest chunk.
-int attend_splits(int64_t units, int64_t len, int64_t min_chunk, int64_t blocks) {
-    int64_t s = (blocks + units - 1) / units;
-    const int64_t most = (len + min_chunk - 1) / min_chunk;
+// Row kernel: slots for `units` (row tile, KV head) pairs over `len` tokens:
+// enough blocks for four per SM, none with less than the smallest chunk.
+int attend_splits(int64_t units, int64_t len) {
+    int64_t s = (kAttendSms * 4 + units - 1) / units;
+    const int64_t most = (len + attend::kMinChunk - 1) / attend::kMinChunk;
     if (s > most) s = most;
     return int(s < 1 ? 1 : s > 256 ? 256 : s);
+}
+
+// Tall kernel, one CTA per SM: the number of slots whose whole waves of CTAs
+// take the fewest tile steps, counting what a CTA does besides (Q, the ends
+// of the pipeline, its partial output) as four.
+int attend_wide_splits(int64_t units, int64_t rows, int64_t len) {
+    const int64_t tiles = (len + attend::kTile - 1) / attend::kTile;
+    const int64_t per_tile = rows > attend::kTile ? 2 : 1;
+    int64_t best = 1, best_cost = INT64_MAX;
+    for (int64_t s = 1; s <= 64 && s <= tiles; ++s) {
+        const int64_t waves = (units * s + kAttendSms - 1) / kAttendSms;
+        const int64_t cost = waves * ((tiles + s - 1) / s * per_tile + 4);
+        if (cost < best_cost) best = s, best_cost = cost;
+    }
+    return int(best);
 }
 
 bool attend_shape_ok(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_len,
@@ -914,12 +933,20 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t 
     AttendPlan a;
     const int64_t G = Hq / Hkv;
     if (prefix_len > 0) {
-        a.tiles_p = (T * G + attend::kRows - 1) / attend::kRows;
-        a.splits_p = attend_splits(a.tiles_p * Hkv, prefix_len, attend::kMinChunk, kAttendSms * 4);
+        const int64_t rows = T * G;
+        a.wide_p = rows >= kWideFrom;
+        const int64_t tile = a.wide_p ? attend::kWideRows : attend::kRows;
+        a.tiles_p = (rows + tile - 1) / tile;
+        a.splits_p = a.wide_p ? attend_wide_splits(a.tiles_p * Hkv, rows, prefix_len)
+                              : attend_splits(a.tiles_p * Hkv, prefix_len);
     }
     if (max_pages > 0 || prefix_len == 0) {
-        a.tiles_o = ((max_q < T ? max_q : T) * G + attend::kRows - 1) / attend::kRows;
-        a.splits_o = attend_splits(a.tiles_o * Hkv * B, max_pages * page_size, attend::kMinChunk, kAttendSms * 4);
+        const int64_t rows = (max_q < T ? max_q : T) * G;
+        a.wide_o = rows >= kWideFrom && max_pages > 0;
+        const int64_t tile = a.wide_o ? attend::kWideRows : attend::kRows;
+        a.tiles_o = (rows + tile - 1) / tile;
+        a.splits_o = a.wide_o ? attend_wide_splits(a.tiles_o * Hkv * B, rows, max_pages * page_size)
+                              : attend_splits(a.tiles_o * Hkv * B, max_pages * page_size);
     }
     const int64_t slots = a.splits_p + a.splits_o;
     a.direct = slots == 1;
@@ -930,23 +957,59 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t 
     return a;
 }
 
+// The codes of a paged cache tensor as rows of D bytes: a copy takes the
+// rows of one head in one page, at most a tile of them, D-byte swizzle.
+mfp8_status make_map_pages(CUtensorMap* map, const void* base, int64_t rows, int64_t D, int box_rows) {
+    cuuint64_t dims[2] = {cuuint64_t(D), cuuint64_t(rows)};
+    cuuint64_t strides[1] = {cuuint64_t(D)};
+    cuuint32_t box[2] = {cuuint32_t(D), cuuint32_t(box_rows)};
+    cuuint32_t estr[2] = {1u, 1u};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MFP8_OK : MFP8_ERR_CUDA;
+}
+
 template <int D>
-mfp8_status launch_attend(const attend::Params& p, int64_t units, int dev, cudaStream_t stream) {
+mfp8_status launch_attend(attend::Params p, const AttendPlan& plan, int dev, cudaStream_t stream) {
     using L = attend::RowsLayout<D>;
+    using WL = attend::WideLayout<D>;
     static bool ready[kMaxDevices] = {};
     {
         std::lock_guard<std::mutex> lock(g_mu);
         if (!ready[dev]) {
             if (cudaFuncSetAttribute(attend::attend_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     L::SMEM) != cudaSuccess) {
+                                     L::SMEM) != cudaSuccess ||
+                cudaFuncSetAttribute(attend::attend_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     WL::SMEM_BYTES) != cudaSuccess) {
                 cudaGetLastError();
                 return MFP8_ERR_CUDA;
             }
             ready[dev] = true;
         }
     }
-    mfp8_status st = launch_pdl(attend::attend_rows_kernel<D>, dim3(unsigned(units)), attend::kThreads, stream, L::SMEM, p);
-    if (st != MFP8_OK || p.direct) return st;
+    const int64_t units_p = plan.tiles_p * plan.splits_p * p.Hkv, units_o = plan.tiles_o * plan.splits_o * p.Hkv * p.B;
+    const int64_t wide = (plan.wide_p ? units_p : 0) + (plan.wide_o ? units_o : 0);
+    const int64_t narrow = units_p + units_o - wide;
+    mfp8_status st = MFP8_OK;
+    if (wide > 0) {
+        const int ps = 1 << p.ps_shift;
+        const int64_t rows = p.n_pages * p.Hkv * ps;
+        CUtensorMap tmK, tmV;
+        if ((st = make_map_pages(&tmK, p.K, rows, D, ps < attend::kTile ? ps : attend::kTile)) != MFP8_OK) return st;
+        if ((st = make_map_pages(&tmV, p.V, rows, D, ps < attend::kTile ? ps : attend::kTile)) != MFP8_OK) return st;
+        const attend::WideGrid wg{plan.wide_p ? int(plan.tiles_p) : 0, plan.wide_o ? int(plan.tiles_o) : 0};
+        st = launch_pdl(attend::attend_wide_kernel<D>, dim3(unsigned(wide)), attend::kWideThreads, stream,
+                        WL::SMEM_BYTES, p, wg, tmK, tmV);
+        if (st != MFP8_OK) return st;
+    }
+    if (narrow > 0) {
+        p.tiles_p = plan.wide_p ? 0 : int(plan.tiles_p);
+        p.tiles_o = plan.wide_o ? 0 : int(plan.tiles_o);
+        st = launch_pdl(attend::attend_rows_kernel<D>, dim3(unsigned(narrow)), attend::kThreads, stream, L::SMEM, p);
+        if (st != MFP8_OK) return st;
+    }
+    if (p.direct) return MFP8_OK;
     const int64_t rows = int64_t(p.T) * p.Hq;
     return launch_pdl(attend::join_kernel<D>, dim3(unsigned((rows + 7) / 8)), 256, stream, 0, p);
 }
@@ -1568,7 +1631,7 @@ mfp8_status mfp8_prefix_attention(const void* Q_bf16, int64_t ldq, int64_t T, in
         for (int i = 0; i < j; ++i)
             if (len[i] && len[j] && ranges_overlap(buf[i], len[i], buf[j], len[j])) return MFP8_ERR_INVALID_ARG;
     const int64_t np = plan.tiles_p * plan.splits_p * Hkv, no = plan.tiles_o * plan.splits_o * Hkv * B;
-    if (np + no > INT32_MAX) return MFP8_ERR_UNSUPPORTED_SHAPE;
+    if (np + no > INT32_MAX || int64_t(rows) > INT32_MAX) return MFP8_ERR_UNSUPPORTED_SHAPE;
     int dev;
     DeviceInfo info;
     mfp8_status st = current_device(&dev, &info);
@@ -1601,12 +1664,10 @@ mfp8_status mfp8_prefix_attention(const void* Q_bf16, int64_t ldq, int64_t T, in
     p.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.lse_off);
     p.splits_p = plan.splits_p;
     p.splits_o = plan.splits_o;
-    p.tiles_p = int(plan.tiles_p);
-    p.tiles_o = int(plan.tiles_o);
     p.max_q = int(max_q);
     p.direct = plan.direct;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return D == 128 ? launch_attend<128>(p, np + no, dev, s) : launch_attend<64>(p, np + no, dev, s);
+    return D == 128 ? launch_attend<128>(p, plan, dev, s) : launch_attend<64>(p, plan, dev, s);
 }
 
 mfp8_status mfp8_debug_kv8_code_check(void* out_u64x2, int64_t n_scale_pairs, uint32_t seed, void* stream) {

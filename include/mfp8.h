@@ -440,10 +440,11 @@ MFP8_API size_t mfp8_prefix_attention_workspace_bytes(int64_t T, int64_t B, int6
  * (a bad page reads page 0), and recorded as MFP8_ERR_INDEX in the device
  * status.  Sums, softmax statistics and partial outputs are fp32; the
  * probabilities times the value scales are rounded to 11 bits (f16 relative
- * to the largest value scale read, so value scales within one call should
- * lie within 2^28 of one another), the outputs once to bf16.
+ * to the largest value scale read, so what a row sees should have value
+ * scales within 2^24 of the largest), the outputs once to bf16.
  * D is 64 or 128; Hq a multiple of Hkv; B, max_q and T up to 2^20, prefix_len
- * and max_pages * page_size up to 2^30.  T == 0 or B == 0 is a no-op. */
+ * and max_pages * page_size up to 2^30, n_pages * Hkv * page_size below 2^31
+ * (a layer of more than 128 GB).  T == 0 or B == 0 is a no-op. */
 MFP8_API mfp8_status mfp8_prefix_attention(const void* Q_bf16, int64_t ldq, int64_t T, int64_t Hq, int64_t Hkv,
                                            int64_t D, const int32_t* q_start, const int32_t* kv_len, int64_t B,
                                            int64_t max_q, const void* k_pages, const float* k_scale,

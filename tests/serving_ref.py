@@ -131,7 +131,8 @@ class Batch:
         same with q's largest element in every place: a logit is a sum of D
         products in fp32 on the tensor cores, each addition off by at most
         2^-23 of the terms' sum (truncated), D <= 128: 2^-16 A; q itself is
-        held to 2^-18 of its row's largest element: 2^-18 C.  Scaling and
+        held to 2^-17 of its row's largest element (two e4m3 terms, half of
+        the smallest step 2^-9 against a largest element of at least 224: 2^-17.8): 2^-17 C.  Scaling and
         exponential add 2^-22 relative and 2^-22 of the logit.  That error dz
         moves a weight by dz and the sum by dz, so a probability by 2 dz.  A
         weight times its value scale is rounded to f16: 2^-11.  The fp32 sums
@@ -164,7 +165,7 @@ class Batch:
                 p = torch.where(seen, torch.exp(z - torch.where(none, 0.0, w)[:, None]), 0.0)
                 o = p @ v
                 if N:
-                    dz = (a * 2.0 ** -16 + c * 2.0 ** -18 + a * 2.0 ** -22).amax(-1) + 2.0 ** -21
+                    dz = (a * 2.0 ** -16 + c * 2.0 ** -17 + a * 2.0 ** -22).amax(-1) + 2.0 ** -21
                 else:
                     dz = torch.zeros(n * G, dtype=torch.float64, device=dev)
                 rel = 2.0 ** -11 + 2 * dz + (N / 16 + 32) * 2.0 ** -22
