@@ -50,7 +50,11 @@ constexpr int kWideThreads = 512;
 constexpr int kTile = 128;      // tokens per tile, rows per side
 constexpr int kWideRows = 256;  // rows per CTA
 constexpr float kLag = 4.0f;
-constexpr int kNorm = 11;  // p < 2^kLag, sv / M <= 1: f16 values below 2^15
+constexpr int kNorm = 11;     // p < 2^kLag, sv / M <= 1: f16 values below 2^15
+constexpr int kMinVexp = 37;  // M >= 2^-90: sums of p 2^kNorm / M stay finite
+// Registers: 512 threads are launched with 128 each; the softmax warps, which
+// hold a row of 128 logits, take 192 and leave 64 to the others.
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
 
 template <int D>
 struct WideLayout {
@@ -126,6 +130,46 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A row's logits times the key scales (in shared memory at `sk`); their maximum.
+__device__ __forceinline__ float scale_logits(uint32_t (&z)[128], uint32_t sk) {
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int q = 0; q < 128; q += 4) {
+        const float4 s = ld_shared_f4(sk + q * 4);
+        float z0, z1, z2, z3;
+        unpack2(mul2(pack2(__uint_as_float(z[q]), __uint_as_float(z[q + 1])), pack2(s.x, s.y)), z0, z1);
+        unpack2(mul2(pack2(__uint_as_float(z[q + 2]), __uint_as_float(z[q + 3])), pack2(s.z, s.w)), z2, z3);
+        z[q] = __float_as_uint(z0), z[q + 1] = __float_as_uint(z1);
+        z[q + 2] = __float_as_uint(z2), z[q + 3] = __float_as_uint(z3);
+        float& a = mx[(q >> 1) & 3];
+        float& b = mx[((q >> 1) + 1) & 3];
+        a = fmaxf(a, fmaxf(z0, z1));
+        b = fmaxf(b, fmaxf(z2, z3));
+    }
+    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
+// The same row with tokens at and past `lim` (token `base` is column 0) out
+// of it, whatever stands there; the maximum of what is left.
+__device__ __forceinline__ float mask_logits(uint32_t (&z)[128], int base, int lim) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < 128; ++q) {
+        if (base + q >= lim) z[q] = 0xff800000u;
+        mx = fmaxf(mx, __uint_as_float(z[q]));
+    }
+    return mx;
+}
 
 // Which part and unit of the grid a CTA works on.
 struct WideGrid {
@@ -219,6 +263,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
 
     if (warp < 8) {
         // ------------------------------------------------------ softmax
+        regs_inc<kSoftmaxRegs>();
         const int side = int(warp >> 2);
         const int i = int(threadIdx.x & 127);
         const int r = r0 + (both ? side * kTile : 0) + i;
@@ -268,7 +313,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         const uint32_t lane_base = tmem + ((warp & 3u) << 21);
         const uint32_t tS = lane_base + uint32_t(side) * 128u, tO = lane_base + 256u + uint32_t(side) * 128u;
         float m = -INFINITY, l = 0.0f;
-        int vexp = 27, n = 0;
+        int vexp = kMinVexp, n = 0;
         const uint64_t f2 = pack2(f, f);
         for (int j = side; j < steps; j += 2, ++n) {
             const int tile = both ? j >> 1 : j;
@@ -278,90 +323,61 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             tc_fence_after();
             const uint32_t sk = sb + L::CS_OFF + cs * 1024;
             const int base = k0 + tile * kTile;
-            const bool masked = base + kTile > all_see;
-            float mx = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t z[32];
-                tmem_ld_32x32b_x32(tS + c * 32, z);
-                tmem_wait_ld();
-#pragma unroll
-                for (int q = 0; q < 32; q += 4) {
-                    const float4 s = ld_shared_f4(sk + (c * 32 + q) * 4);
-                    float z0 = __uint_as_float(z[q]) * s.x, z1 = __uint_as_float(z[q + 1]) * s.y;
-                    float z2 = __uint_as_float(z[q + 2]) * s.z, z3 = __uint_as_float(z[q + 3]) * s.w;
-                    if (masked) {
-                        const int tok = base + c * 32 + q;
-                        if (tok >= lim) z0 = -INFINITY;
-                        if (tok + 1 >= lim) z1 = -INFINITY;
-                        if (tok + 2 >= lim) z2 = -INFINITY;
-                        if (tok + 3 >= lim) z3 = -INFINITY;
-                    }
-                    mx = fmaxf(fmaxf(mx, fmaxf(z0, z1)), fmaxf(z2, z3));
-                }
-            }
-            mx *= f;
             // the largest value scale of the tile, as a power of two above it
             const uint4 ve4 = lds128(sb + L::VE_OFF + cs * 16);
             const int ve = max(vexp, min(int(max(max(ve4.x, ve4.y), max(ve4.z, ve4.w)) >> 23) + 1, 254));
+            uint32_t z[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(z + c * 32));
+            tmem_wait_ld();
+            float mx = scale_logits(z, sk);
+            if (base + kTile > all_see) mx = mask_logits(z, base, lim);
+            mx *= f;
             // m = -inf (nothing seen yet) has -inf + kLag below every finite maximum
             if (__any_sync(0xffffffffu, mx > m + kLag || ve != vexp)) {
                 const float mn = fmaxf(m, mx);
-                const float keep = mn == -INFINITY ? 1.0f : ex2(m - mn);
+                const float keep = (mn == -INFINITY ? 1.0f : ex2(m - mn)) * pow2i(max(vexp - ve, -126));
                 m = mn;
+                vexp = ve;
                 l *= keep;
                 if (n > 0) {
-                    const float scale = keep * pow2i(max(vexp - ve, -126));
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
                         tmem_ld_32x32b_x32(tO + c * 32, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * scale);
+                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * keep);
                         tmem_st_32x32b_x32(tO + c * 32, o);
                     }
                 }
-                vexp = ve;
             }
-            const float mz = m == -INFINITY ? 0.0f : m;
-            const uint64_t nm2 = pack2(-mz, -mz);
-            const float vn = pow2i(kNorm - (vexp - 127));
-            const uint64_t vn2 = pack2(vn, vn);
-            uint64_t sum2 = pack2(0.0f, 0.0f);
+            // p 2^kNorm / M = 2^(z - m + kNorm - log2 M), summed as it is
+            const float off = float(kNorm + 127 - vexp) - (m == -INFINITY ? 0.0f : m);
+            const uint64_t off2 = pack2(off, off);
+            uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};  // pairs of +0
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                uint32_t z[32], w[16];
-                tmem_ld_32x32b_x32(tS + c * 32, z);
-                tmem_wait_ld();
+                uint32_t w[16];
 #pragma unroll
                 for (int q = 0; q < 32; q += 4) {
-                    const float4 s = ld_shared_f4(sk + (c * 32 + q) * 4);
                     const float4 v = ld_shared_f4(sk + 512 + (c * 32 + q) * 4);
                     float z0, z1, z2, z3;
-                    uint64_t a = mul2(pack2(__uint_as_float(z[q]), __uint_as_float(z[q + 1])), pack2(s.x, s.y));
-                    uint64_t b = mul2(pack2(__uint_as_float(z[q + 2]), __uint_as_float(z[q + 3])), pack2(s.z, s.w));
-                    unpack2(fma2(a, f2, nm2), z0, z1);
-                    unpack2(fma2(b, f2, nm2), z2, z3);
-                    if (masked) {
-                        const int tok = base + c * 32 + q;
-                        if (tok >= lim) z0 = -INFINITY;
-                        if (tok + 1 >= lim) z1 = -INFINITY;
-                        if (tok + 2 >= lim) z2 = -INFINITY;
-                        if (tok + 3 >= lim) z3 = -INFINITY;
-                    }
-                    a = pack2(ex2(z0), ex2(z1));
-                    b = pack2(ex2(z2), ex2(z3));
-                    sum2 = add2(sum2, add2(a, b));
-                    unpack2(mul2(mul2(a, vn2), pack2(v.x, v.y)), z0, z1);
-                    unpack2(mul2(mul2(b, vn2), pack2(v.z, v.w)), z2, z3);
+                    const uint32_t* zz = z + c * 32 + q;
+                    unpack2(fma2(pack2(__uint_as_float(zz[0]), __uint_as_float(zz[1])), f2, off2), z0, z1);
+                    unpack2(fma2(pack2(__uint_as_float(zz[2]), __uint_as_float(zz[3])), f2, off2), z2, z3);
+                    const uint64_t a = pack2(ex2(z0), ex2(z1)), b = pack2(ex2(z2), ex2(z3));
+                    sum2[(q >> 1) & 3] = add2(sum2[(q >> 1) & 3], a);
+                    sum2[((q >> 1) + 1) & 3] = add2(sum2[((q >> 1) + 1) & 3], b);
+                    unpack2(mul2(a, pack2(v.x, v.y)), z0, z1);
+                    unpack2(mul2(b, pack2(v.z, v.w)), z2, z3);
                     w[q / 2] = pack_f16x2(z0, z1);
                     w[q / 2 + 1] = pack_f16x2(z2, z3);
                 }
-                tmem_st_32x32b_x16(tS + c * 16, w);  // over columns of z that have been read
+                tmem_st_32x32b_x16(tS + c * 16, w);
             }
             float s0, s1;
-            unpack2(sum2, s0, s1);
+            unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])), s0, s1);
             l += s0 + s1;
             tmem_wait_st();
             tc_fence_before();
@@ -373,8 +389,9 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         bool ok = mine > 0 && n == mine && mbar_wait(bar(L::OFULL + side), 0, abort_flag);
         if (!both && side == 1 && ok) ok = mbar_wait(bar(L::OFULL), 0, abort_flag);  // every MMA is done
         tc_fence_after();
-        const float inv = ok && l > 0.0f ? ldexpf(1.0f / l, vexp - 127 - kNorm) : 0.0f;
-        float my_lse = ok && l > 0.0f ? m + log2f(l) : -INFINITY;
+        // O and l carry the same factor 2^kNorm / M
+        const float inv = ok && l > 0.0f ? 1.0f / l : 0.0f;
+        float my_lse = ok && l > 0.0f ? m + (log2f(l) - float(kNorm + 127 - vexp)) : -INFINITY;
         float* buf = reinterpret_cast<float*>(smem + L::Q_OFF);  // [D][128]: side 1's output when joined
         float* lbuf = reinterpret_cast<float*>(smem + L::LSE_OFF);
         float w0 = 1.0f, w1 = 0.0f;
@@ -443,6 +460,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         }
     } else if (warp < 12) {
         // ------------------------------------------- V: e4m3 to f16
+        regs_dec<kOtherRegs>();
         const int tid = int(threadIdx.x) - 256;
         constexpr int CH = D / 16;        // 16-code pieces per token
         constexpr int RPI = 128 / CH;     // tokens per pass
@@ -494,7 +512,9 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
                 mbar_arrive(bar(L::VEMPTY + vs));
             }
         }
-    } else if (warp == 12) {
+    } else {
+        regs_dec<kOtherRegs>();
+        if (warp == 12) {
         // -------------------------------------------------------- loads
         const int ps = 1 << p.ps_shift;
         const int box = min(ps, kTile);       // rows of one copy
@@ -537,7 +557,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
                 mbar_wait(bar(L::VFULL + t % L::VST), (t / L::VST) & 1, &no_abort, 10000000ull);
             }
         }
-    } else if (warp == 13 && lane == 0) {
+        } else if (warp == 13 && lane == 0) {
         // ---------------------------------------------------------- MMA
         constexpr uint32_t idesc_s = idesc_e4m3_f32(128, kTile);
         constexpr uint32_t idesc_o = idesc_pv(D);
@@ -589,6 +609,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             volatile int no_abort = 0;
             mma_commit(bar(L::DRAIN));
             mbar_wait(bar(L::DRAIN), 0, &no_abort, 10000000ull);
+        }
         }
     }
 
