@@ -50,8 +50,9 @@ constexpr int kWideThreads = 512;
 constexpr int kTile = 128;      // tokens per tile, rows per side
 constexpr int kWideRows = 256;  // rows per CTA
 constexpr float kLag = 4.0f;
-constexpr int kNorm = 11;     // p < 2^kLag, sv / M <= 1: f16 values below 2^15
-constexpr int kMinVexp = 37;  // M >= 2^-90: sums of p 2^kNorm / M stay finite
+constexpr int kNorm = 11;     // P holds p 2^kNorm, below 2^15 in f16
+constexpr int kVNorm = 7;     // V holds dec(V) sv / M 2^kVNorm, below 448 * 2^7
+constexpr int kMinVexp = 27;  // M >= 2^-100
 // Registers: 512 threads are launched with 128 each; the softmax warps, which
 // hold a row of 128 logits, take 192 and leave 64 to the others.
 constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
@@ -64,13 +65,13 @@ struct WideLayout {
     static constexpr int K_OFF = Q_OFF + 4 * QB;
     static constexpr int V_OFF = K_OFF + KST * kTile * D;
     static constexpr int C_OFF = V_OFF + VST * kTile * D;       // f16 V: [dim / 64][token][64 dims]
-    static constexpr int VS_OFF = C_OFF + CST * kTile * D * 2;  // scales as loaded: sk, sv
-    static constexpr int CS_OFF = VS_OFF + VST * 1024;          // scales for the softmax: sk, sv (0 past the end)
-    static constexpr int VE_OFF = CS_OFF + CST * 1024;          // largest sv's bits of each converting warp
-    static constexpr int BAR_OFF = VE_OFF + CST * 16;
+    static constexpr int SST = 4;
+    static constexpr int S_OFF = C_OFF + CST * kTile * D * 2;  // key scales, value scales
+    static constexpr int BAR_OFF = S_OFF + SST * 1024;
     static constexpr int KFULL = 0, KEMPTY = KST, VFULL = 2 * KST, VEMPTY = VFULL + VST, CFULL = VEMPTY + VST,
-                         CEMPTY = CFULL + CST, SFULL = CEMPTY + CST, PFULL = SFULL + 2, OFULL = PFULL + 2,
-                         QFULL = OFULL + 2, DRAIN = QFULL + 1, NUM_BARS = DRAIN + 1;
+                         CEMPTY = CFULL + CST, LFULL = CEMPTY + CST, LEMPTY = LFULL + SST, SFULL = LEMPTY + SST,
+                         PFULL = SFULL + 2, OFULL = PFULL + 2, QFULL = OFULL + 2, DRAIN = QFULL + 1,
+                         NUM_BARS = DRAIN + 1;
     static constexpr int LSE_OFF = BAR_OFF + NUM_BARS * 8;  // [128] log-sum-exps of side 1 at the end
     static constexpr int MISC_OFF = LSE_OFF + 512;
     static constexpr int USED = MISC_OFF + 16;
@@ -171,6 +172,16 @@ __device__ __forceinline__ float mask_logits(uint32_t (&z)[128], int base, int l
     return mx;
 }
 
+// log2 of M, biased: a power of two above `before` and above the value scales
+// (in shared memory at `sv`) of the tile's `valid` tokens.  Whole warp.
+__device__ __forceinline__ int tile_vexp(int before, uint32_t sv, int valid, int lane) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int q = 0; q < kTile / 32; ++q)
+        if (lane + 32 * q < valid) top = max(top, __float_as_uint(ld_shared_f32(sv + (lane + 32 * q) * 4)));
+    return max(before, min(int(__reduce_max_sync(0xffffffffu, top) >> 23) + 1, 254));
+}
+
 // Which part and unit of the grid a CTA works on.
 struct WideGrid {
     int pairs_p, pairs_o;  // 256-row groups of the prefix's rows, of one sequence's rows
@@ -245,6 +256,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             if (i >= L::CFULL && i < L::CFULL + L::CST) n = 4;
             if (i >= L::PFULL && i < L::PFULL + 2) n = 4;  // softmax warps of the side
             if (i == L::QFULL) n = 8;
+            if (i >= L::LEMPTY && i < L::LEMPTY + L::SST) n = both ? 12 : 8;  // softmax warps of the tile's sides, converters
             mbar_init(bar(i), n);
         }
         *abort_flag = 0;
@@ -274,9 +286,12 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         {
             const uint4* q = reinterpret_cast<const uint4*>(p.Q + int64_t(k.tok0 + t) * p.ldq +
                                                             int64_t(h * p.G + (live ? r % p.G : 0)) * D);
+            uint4 x8[D / 8];  // every load of the row in flight at once
             uint32_t acc = 0;
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) acc = absmax_bits_u4(live ? q[c] : make_uint4(0u, 0u, 0u, 0u), acc);
+            for (int c = 0; c < D / 8; ++c) x8[c] = live ? __ldg(q + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) acc = absmax_bits_u4(x8[c], acc);
             const uint32_t amax = max(acc & 0xffffu, acc >> 16);
             // 2^e puts the largest element in [224, 448]: its exponent at 8, or at 7 above 1.75 * 2^n
             int e = max(int(amax >> 7), 10) - 127 - 8;
@@ -285,10 +300,9 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             f = fmaxf(p.scale_log2 * pow2i(e), kFltMin);
             const uint32_t hi = sb + L::Q_OFF + side * 2 * L::QB + i * D, lo = hi + L::QB;
             const uint32_t x = D == 128 ? uint32_t(i & 7) : uint32_t((i >> 1) & 3);
-#pragma unroll 2
+#pragma unroll
             for (int c = 0; c < D / 16; ++c) {
-                const uint4 a = live ? q[2 * c] : make_uint4(0u, 0u, 0u, 0u);
-                const uint4 b = live ? q[2 * c + 1] : make_uint4(0u, 0u, 0u, 0u);
+                const uint4 a = x8[2 * c], b = x8[2 * c + 1];
                 const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
                 uint32_t ch[4] = {0u, 0u, 0u, 0u}, cl[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -317,29 +331,30 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         const uint64_t f2 = pack2(f, f);
         for (int j = side; j < steps; j += 2, ++n) {
             const int tile = both ? j >> 1 : j;
-            const int cs = tile % L::CST;
-            if (!mbar_wait(bar(L::CFULL + cs), (tile / L::CST) & 1, abort_flag)) break;
+            const int ls = tile % L::SST;
+            const int base = k0 + tile * kTile;
+            if (!mbar_wait(bar(L::LFULL + ls), (tile / L::SST) & 1, abort_flag)) break;
+            const uint32_t sk = sb + L::S_OFF + ls * 1024;
+            const int ve = tile_vexp(vexp, sk + 512, min(kTile, k1 - base), lane);
             if (!mbar_wait(bar(L::SFULL + side), n & 1, abort_flag)) break;
             tc_fence_after();
-            const uint32_t sk = sb + L::CS_OFF + cs * 1024;
-            const int base = k0 + tile * kTile;
-            // the largest value scale of the tile, as a power of two above it
-            const uint4 ve4 = lds128(sb + L::VE_OFF + cs * 16);
-            const int ve = max(vexp, min(int(max(max(ve4.x, ve4.y), max(ve4.z, ve4.w)) >> 23) + 1, 254));
             uint32_t z[128];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(z + c * 32));
             tmem_wait_ld();
             float mx = scale_logits(z, sk);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::LEMPTY + ls));
             if (base + kTile > all_see) mx = mask_logits(z, base, lim);
             mx *= f;
             // m = -inf (nothing seen yet) has -inf + kLag below every finite maximum
             if (__any_sync(0xffffffffu, mx > m + kLag || ve != vexp)) {
                 const float mn = fmaxf(m, mx);
-                const float keep = (mn == -INFINITY ? 1.0f : ex2(m - mn)) * pow2i(max(vexp - ve, -126));
+                float keep = mn == -INFINITY ? 1.0f : ex2(m - mn);
                 m = mn;
-                vexp = ve;
                 l *= keep;
+                keep *= pow2i(max(vexp - ve, -126));
+                vexp = ve;
                 if (n > 0) {
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
@@ -352,8 +367,8 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
                     }
                 }
             }
-            // p 2^kNorm / M = 2^(z - m + kNorm - log2 M), summed as it is
-            const float off = float(kNorm + 127 - vexp) - (m == -INFINITY ? 0.0f : m);
+            // p 2^kNorm = 2^(z - m + kNorm), summed as it is
+            const float off = float(kNorm) - (m == -INFINITY ? 0.0f : m);
             const uint64_t off2 = pack2(off, off);
             uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};  // pairs of +0
 #pragma unroll
@@ -361,16 +376,13 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
                 uint32_t w[16];
 #pragma unroll
                 for (int q = 0; q < 32; q += 4) {
-                    const float4 v = ld_shared_f4(sk + 512 + (c * 32 + q) * 4);
                     float z0, z1, z2, z3;
                     const uint32_t* zz = z + c * 32 + q;
                     unpack2(fma2(pack2(__uint_as_float(zz[0]), __uint_as_float(zz[1])), f2, off2), z0, z1);
                     unpack2(fma2(pack2(__uint_as_float(zz[2]), __uint_as_float(zz[3])), f2, off2), z2, z3);
-                    const uint64_t a = pack2(ex2(z0), ex2(z1)), b = pack2(ex2(z2), ex2(z3));
-                    sum2[(q >> 1) & 3] = add2(sum2[(q >> 1) & 3], a);
-                    sum2[((q >> 1) + 1) & 3] = add2(sum2[((q >> 1) + 1) & 3], b);
-                    unpack2(mul2(a, pack2(v.x, v.y)), z0, z1);
-                    unpack2(mul2(b, pack2(v.z, v.w)), z2, z3);
+                    z0 = ex2(z0), z1 = ex2(z1), z2 = ex2(z2), z3 = ex2(z3);
+                    sum2[(q >> 1) & 3] = add2(sum2[(q >> 1) & 3], pack2(z0, z1));
+                    sum2[((q >> 1) + 1) & 3] = add2(sum2[((q >> 1) + 1) & 3], pack2(z2, z3));
                     w[q / 2] = pack_f16x2(z0, z1);
                     w[q / 2 + 1] = pack_f16x2(z2, z3);
                 }
@@ -385,13 +397,15 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             if (lane == 0) mbar_arrive(bar(L::PFULL + side));
         }
         // ---- the output of this side's tiles
+        const int64_t my_row = live ? row_of(r) : 0;
         const int mine = both ? nt : (nt + 1 - side) / 2;
         bool ok = mine > 0 && n == mine && mbar_wait(bar(L::OFULL + side), 0, abort_flag);
         if (!both && side == 1 && ok) ok = mbar_wait(bar(L::OFULL), 0, abort_flag);  // every MMA is done
         tc_fence_after();
-        // O and l carry the same factor 2^kNorm / M
-        const float inv = ok && l > 0.0f ? 1.0f / l : 0.0f;
-        float my_lse = ok && l > 0.0f ? m + (log2f(l) - float(kNorm + 127 - vexp)) : -INFINITY;
+        // l carries 2^kNorm, O that and 2^kVNorm / M
+        const bool any = ok && m > -INFINITY;
+        const float inv = any ? ldexpf(1.0f / l, vexp - 127 - kVNorm) : 0.0f;
+        float my_lse = any ? m + (log2f(l) - float(kNorm)) : -INFINITY;
         float* buf = reinterpret_cast<float*>(smem + L::Q_OFF);  // [D][128]: side 1's output when joined
         float* lbuf = reinterpret_cast<float*>(smem + L::LSE_OFF);
         float w0 = 1.0f, w1 = 0.0f;
@@ -423,73 +437,85 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             }
         }
         if (both || side == 0) {  // uniform over the warp, as tcgen05.ld wants
-            // O is finite wherever this side had a tile (its P is 0 for what it does not see)
-            const int64_t row = live ? row_of(r) : 0;
+            // O is finite wherever this side had a tile (its P is 0 for what it does not see).  A row per thread
+            // would be stored 16 bytes at a time to 32 places; through shared memory (4 KB per warp that no MMA
+            // reads any more, 16-byte pieces swizzled by row) four rows leave as 128 contiguous bytes each.
             const float s = inv * w0;
-#pragma unroll
+            const uint32_t stage = sb + (join ? L::K_OFF : L::Q_OFF + side * 2 * L::QB) + (warp & 3u) * 4096u;
+            const int rbase = r0 + (both ? side * kTile : 0) + int(warp & 3u) * 32;
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
-                float y[32];
                 tmem_ld_32x32b_x32(tO + c * 32, o);
                 tmem_wait_ld();
+                __syncwarp();  // the chunk before has been read
 #pragma unroll
-                for (int q = 0; q < 32; ++q) {
-                    y[q] = __uint_as_float(o[q]) * s;
-                    if (join) y[q] = fmaf(buf[(c * 32 + q) * 128 + i], w1, y[q]);
-                }
-                if (live && p.direct) {
-                    uint4* dst = reinterpret_cast<uint4*>(p.O + row * D + c * 32);
+                for (int q = 0; q < 32; q += 4) {
+                    float y[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t pk[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(y[8 * q + 2 * e], y[8 * q + 2 * e + 1]);
-                            pk[e] = *reinterpret_cast<const uint32_t*>(&b);
-                        }
-                        dst[q] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    for (int e = 0; e < 4; ++e) {
+                        y[e] = __uint_as_float(o[q + e]) * s;
+                        if (join) y[e] = fmaf(buf[(c * 32 + q + e) * 128 + i], w1, y[e]);
                     }
-                } else if (live) {
-                    float4* dst = reinterpret_cast<float4*>(p.part + (int64_t(slot) * all_rows + row) * D + c * 32);
+                    st_shared_v4(stage + lane * 128 + (((q >> 2) ^ (lane & 7)) << 4), __float_as_uint(y[0]),
+                                 __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+                }
+                __syncwarp();
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) dst[q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+                for (int a = 0; a < 8; ++a) {
+                    const int rr = 4 * a + (lane >> 3), piece = lane & 7;
+                    const float4 y = ld_shared_f4(stage + rr * 128 + ((piece ^ (rr & 7)) << 4));
+                    const int64_t row = __shfl_sync(0xffffffffu, my_row, rr);
+                    if (rbase + rr < nrows) {
+                        const int64_t at = row * D + c * 32 + piece * 4;
+                        if (p.direct) {
+                            const __nv_bfloat162 b0 = __floats2bfloat162_rn(y.x, y.y), b1 = __floats2bfloat162_rn(y.z, y.w);
+                            *reinterpret_cast<uint2*>(p.O + at) =
+                                make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+                        } else {
+                            *reinterpret_cast<float4*>(p.part + int64_t(slot) * all_rows * D + at) = y;
+                        }
+                    }
                 }
             }
-            if (live && !p.direct) p.part_lse[int64_t(slot) * all_rows + row] = my_lse;
-            else if (live && p.lse) p.lse[row] = my_lse == -INFINITY ? -INFINITY : my_lse * kLn2;
+            if (live && !p.direct) p.part_lse[int64_t(slot) * all_rows + my_row] = my_lse;
+            else if (live && p.lse) p.lse[my_row] = my_lse == -INFINITY ? -INFINITY : my_lse * kLn2;
         }
     } else if (warp < 12) {
         // ------------------------------------------- V: e4m3 to f16
         regs_dec<kOtherRegs>();
         const int tid = int(threadIdx.x) - 256;
-        constexpr int CH = D / 16;        // 16-code pieces per token
-        constexpr int RPI = 128 / CH;     // tokens per pass
+        constexpr int CH = D / 16;     // 16-code pieces per token
+        constexpr int RPI = 128 / CH;  // tokens per pass
         const int ch = tid % CH;
+        int vexp[2] = {kMinVexp, kMinVexp};  // of each side when they take alternate tiles
         for (int tile = 0; tile < nt; ++tile) {
             const int vs = tile % L::VST, cs = tile % L::CST;
             const int valid = min(kTile, k1 - (k0 + tile * kTile));
             if (!mbar_wait(bar(L::VFULL + vs), (tile / L::VST) & 1, abort_flag)) break;
             if (!mbar_wait(bar(L::CEMPTY + cs), ((tile / L::CST) & 1) ^ 1, abort_flag)) break;
             const uint32_t src = sb + L::V_OFF + vs * kTile * D, dst = sb + L::C_OFF + cs * kTile * D * 2;
-            const float skv = ld_shared_f32(sb + L::VS_OFF + vs * 1024 + tid * 4);
-            const float svv = tid < valid ? ld_shared_f32(sb + L::VS_OFF + vs * 1024 + 512 + tid * 4) : 0.0f;
-            float* sc = reinterpret_cast<float*>(smem + L::CS_OFF + cs * 1024);
-            sc[tid] = skv;  // columns past the end are masked by the softmax
-            sc[128 + tid] = svv;
-            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(svv));
-            if (lane == 0) reinterpret_cast<uint32_t*>(smem + L::VE_OFF + cs * 16)[warp - 8] = top;
-#pragma unroll
-            for (int a = 0; a < CH; ++a) {
+            const int ls = tile % L::SST;
+            if (!mbar_wait(bar(L::LFULL + ls), (tile / L::SST) & 1, abort_flag)) break;
+            const uint32_t sc = sb + L::S_OFF + ls * 1024;
+            const int ve = tile_vexp(vexp[both ? 0 : tile & 1], sc + 512, valid, lane);
+            vexp[both ? 0 : tile & 1] = ve;
+            const float inv = pow2i(kVNorm + 127 - ve);
+#pragma unroll 4
+            for (int a = 0; a < kTile / RPI; ++a) {
                 const int row = a * RPI + tid / CH;
                 const uint32_t x = D == 128 ? uint32_t(row & 7) : uint32_t((row >> 1) & 3);
                 uint4 v = lds128(src + row * D + ((uint32_t(ch) ^ x) << 4));
-                if (row >= valid) v = make_uint4(0u, 0u, 0u, 0u);  // whatever the page holds there, NaN codes too
+                float s = ld_shared_f32(sc + 512 + row * 4) * inv;
+                if (row >= valid) v = make_uint4(0u, 0u, 0u, 0u), s = 0.0f;  // whatever the page holds there, NaN too
+                const __half2 s2 = __float2half2_rn(s);
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 uint32_t o[8];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    o[2 * q] = f16x2_of_codes(uint16_t(w[q] & 0xffffu));
-                    o[2 * q + 1] = f16x2_of_codes(uint16_t(w[q] >> 16));
+                for (int q = 0; q < 8; ++q) {
+                    const uint32_t h2 = f16x2_of_codes(uint16_t(q & 1 ? w[q >> 1] >> 16 : w[q >> 1] & 0xffffu));
+                    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h2), s2);
+                    o[q] = *reinterpret_cast<const uint32_t*>(&r);
                 }
                 // 32 bytes: pieces 2 (ch % 4) and + 1 of the row in block ch / 4; the lanes of the other block
                 // write theirs in the other order, so that eight lanes touch eight pieces
@@ -510,6 +536,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             if (lane == 0) {
                 mbar_arrive(bar(L::CFULL + cs));
                 mbar_arrive(bar(L::VEMPTY + vs));
+                mbar_arrive(bar(L::LEMPTY + ls));
             }
         }
     } else {
@@ -536,16 +563,21 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             if (lane == 0) mbar_arrive_expect_tx(bar(L::KFULL + ks), uint32_t(copies * box * D));
             __syncwarp();
             if (lane < copies) tma_load_2d(sb + L::K_OFF + ks * kTile * D + lane * box * D, &tmK, bar(L::KFULL + ks), 0, row);
-            ok = mbar_wait(bar(L::VEMPTY + vs), ((tile / L::VST) & 1) ^ 1, abort_flag);
+            const int ls = tile % L::SST;
+            ok = mbar_wait(bar(L::LEMPTY + ls), ((tile / L::SST) & 1) ^ 1, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) break;
-            if (lane == 0) mbar_arrive_expect_tx(bar(L::VFULL + vs), uint32_t(copies * box * (D + 8)));
+            if (lane == 0) mbar_arrive_expect_tx(bar(L::LFULL + ls), uint32_t(copies * box * 8));
             __syncwarp();
             if (lane < copies) {
-                tma_load_2d(sb + L::V_OFF + vs * kTile * D + lane * box * D, &tmV, bar(L::VFULL + vs), 0, row);
-                const uint32_t sc = sb + L::VS_OFF + vs * 1024 + lane * box * 4;
-                bulk_load(sc, p.k_scale + row, uint32_t(box * 4), bar(L::VFULL + vs));
-                bulk_load(sc + 512, p.v_scale + row, uint32_t(box * 4), bar(L::VFULL + vs));
+                const uint32_t sc = sb + L::S_OFF + ls * 1024 + lane * box * 4;
+                bulk_load(sc, p.k_scale + row, uint32_t(box * 4), bar(L::LFULL + ls));
+                bulk_load(sc + 512, p.v_scale + row, uint32_t(box * 4), bar(L::LFULL + ls));
             }
+            ok = mbar_wait(bar(L::VEMPTY + vs), ((tile / L::VST) & 1) ^ 1, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (lane == 0) mbar_arrive_expect_tx(bar(L::VFULL + vs), uint32_t(copies * box * D));
+            __syncwarp();
+            if (lane < copies) tma_load_2d(sb + L::V_OFF + vs * kTile * D + lane * box * D, &tmV, bar(L::VFULL + vs), 0, row);
             page = next;
             ++issued;
         }
@@ -554,6 +586,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             volatile int no_abort = 0;
             for (int t = max(issued - 3, 0); t <= issued && t < nt; ++t) {
                 mbar_wait(bar(L::KFULL + t % L::KST), (t / L::KST) & 1, &no_abort, 10000000ull);
+                mbar_wait(bar(L::LFULL + t % L::SST), (t / L::SST) & 1, &no_abort, 10000000ull);
                 mbar_wait(bar(L::VFULL + t % L::VST), (t / L::VST) & 1, &no_abort, 10000000ull);
             }
         }
@@ -565,8 +598,6 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         int done[2] = {0, 0};  // P tiles consumed by each side
         auto pv = [&](int side, int tile) {
             if (!mbar_wait(bar(L::PFULL + side), done[side] & 1, abort_flag)) return false;
-            // CFULL needs no wait here: the side's softmax, which PFULL follows, waited for it; but the MMA's
-            // reads are ordered behind the converting warps only through this thread's own wait
             if (!mbar_wait(bar(L::CFULL + tile % L::CST), (tile / L::CST) & 1, abort_flag)) return false;
             tc_fence_after();
             const uint32_t v = sb + L::C_OFF + (tile % L::CST) * kTile * D * 2;

@@ -134,8 +134,9 @@ class Batch:
         held to 2^-17 of its row's largest element (two e4m3 terms, half of
         the smallest step 2^-9 against a largest element of at least 224: 2^-17.8): 2^-17 C.  Scaling and
         exponential add 2^-22 relative and 2^-22 of the logit.  That error dz
-        moves a weight by dz and the sum by dz, so a probability by 2 dz.  A
-        weight times its value scale is rounded to f16: 2^-11.  The fp32 sums
+        moves a weight by dz and the sum by dz, so a probability by 2 dz.  The
+        weight, the value scale and the scaled value are each rounded to f16
+        (or the weight times the value scale once): 3 * 2^-11.  The fp32 sums
         over N tokens, 16 to an addition, are off by (N / 16 + 32) 2^-22 of
         the sum of magnitudes; and the output is rounded to bf16: 2^-8."""
         dev = self.q.device
@@ -168,7 +169,7 @@ class Batch:
                     dz = (a * 2.0 ** -16 + c * 2.0 ** -17 + a * 2.0 ** -22).amax(-1) + 2.0 ** -21
                 else:
                     dz = torch.zeros(n * G, dtype=torch.float64, device=dev)
-                rel = 2.0 ** -11 + 2 * dz + (N / 16 + 32) * 2.0 ** -22
+                rel = 3 * 2.0 ** -11 + 2 * dz + (N / 16 + 32) * 2.0 ** -22
                 t = o.abs() * 2.0 ** -8 + rel[:, None] * (p @ v.abs())
                 shape = (n, G, self.D)
                 out[r, h * G:(h + 1) * G] = o.view(shape)
