@@ -33,7 +33,7 @@
 // The MMAs of a thread run in order, so Q K^T of a side's next tile may
 // overwrite its P as soon as P V has been issued.
 //
-// Every wait is bounded (mbar_wait), as in the GEMM kernels.
+// Every wait is bounded (wait_asleep), as in the GEMM kernels.
 #pragma once
 
 #include <cstdint>
@@ -131,6 +131,35 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// mbar_wait with a long suspend hint (1 ms): a waiting thread sleeps in
+// hardware until its phase completes.  Polling is what the pipeline does not
+// stand: with a bare try_wait loop in the MMA lane alone a step took 1.48 us
+// instead of 1.17.  Bounded like mbar_wait.
+__device__ __forceinline__ bool wait_asleep(uint32_t bar, uint32_t parity, volatile int* abort) {
+    auto attempt = [&] {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(1000000u)
+            : "memory");
+        return ok != 0;
+    };
+    if (attempt()) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (attempt()) return true;
+        if (*abort) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            record_device_status(MFP8_ERR_TIMEOUT);
+            return false;
+        }
+    }
+}
 
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -333,10 +362,10 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             const int tile = both ? j >> 1 : j;
             const int ls = tile % L::SST;
             const int base = k0 + tile * kTile;
-            if (!mbar_wait(bar(L::LFULL + ls), (tile / L::SST) & 1, abort_flag)) break;
+            if (!wait_asleep(bar(L::LFULL + ls), (tile / L::SST) & 1, abort_flag)) break;
             const uint32_t sk = sb + L::S_OFF + ls * 1024;
             const int ve = tile_vexp(vexp, sk + 512, min(kTile, k1 - base), lane);
-            if (!mbar_wait(bar(L::SFULL + side), n & 1, abort_flag)) break;
+            if (!wait_asleep(bar(L::SFULL + side), n & 1, abort_flag)) break;
             tc_fence_after();
             uint32_t z[128];
 #pragma unroll
@@ -399,8 +428,8 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         // ---- the output of this side's tiles
         const int64_t my_row = live ? row_of(r) : 0;
         const int mine = both ? nt : (nt + 1 - side) / 2;
-        bool ok = mine > 0 && n == mine && mbar_wait(bar(L::OFULL + side), 0, abort_flag);
-        if (!both && side == 1 && ok) ok = mbar_wait(bar(L::OFULL), 0, abort_flag);  // every MMA is done
+        bool ok = mine > 0 && n == mine && wait_asleep(bar(L::OFULL + side), 0, abort_flag);
+        if (!both && side == 1 && ok) ok = wait_asleep(bar(L::OFULL), 0, abort_flag);  // every MMA is done
         tc_fence_after();
         // l carries 2^kNorm, O that and 2^kVNorm / M
         const bool any = ok && m > -INFINITY;
@@ -492,11 +521,11 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         for (int tile = 0; tile < nt; ++tile) {
             const int vs = tile % L::VST, cs = tile % L::CST;
             const int valid = min(kTile, k1 - (k0 + tile * kTile));
-            if (!mbar_wait(bar(L::VFULL + vs), (tile / L::VST) & 1, abort_flag)) break;
-            if (!mbar_wait(bar(L::CEMPTY + cs), ((tile / L::CST) & 1) ^ 1, abort_flag)) break;
+            if (!wait_asleep(bar(L::VFULL + vs), (tile / L::VST) & 1, abort_flag)) break;
+            if (!wait_asleep(bar(L::CEMPTY + cs), ((tile / L::CST) & 1) ^ 1, abort_flag)) break;
             const uint32_t src = sb + L::V_OFF + vs * kTile * D, dst = sb + L::C_OFF + cs * kTile * D * 2;
             const int ls = tile % L::SST;
-            if (!mbar_wait(bar(L::LFULL + ls), (tile / L::SST) & 1, abort_flag)) break;
+            if (!wait_asleep(bar(L::LFULL + ls), (tile / L::SST) & 1, abort_flag)) break;
             const uint32_t sc = sb + L::S_OFF + ls * 1024;
             const int ve = tile_vexp(vexp[both ? 0 : tile & 1], sc + 512, valid, lane);
             vexp[both ? 0 : tile & 1] = ve;
@@ -558,13 +587,13 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             const int base = k0 + tile * kTile;
             const int copies = min(per, (k1 - base + box - 1) / box);
             const int32_t row = int32_t(((int64_t(page) * p.Hkv + h) << p.ps_shift) + (base & (ps - 1)));
-            bool ok = mbar_wait(bar(L::KEMPTY + ks), ((tile / L::KST) & 1) ^ 1, abort_flag);
+            bool ok = wait_asleep(bar(L::KEMPTY + ks), ((tile / L::KST) & 1) ^ 1, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) break;
             if (lane == 0) mbar_arrive_expect_tx(bar(L::KFULL + ks), uint32_t(copies * box * D));
             __syncwarp();
             if (lane < copies) tma_load_2d(sb + L::K_OFF + ks * kTile * D + lane * box * D, &tmK, bar(L::KFULL + ks), 0, row);
             const int ls = tile % L::SST;
-            ok = mbar_wait(bar(L::LEMPTY + ls), ((tile / L::SST) & 1) ^ 1, abort_flag);
+            ok = wait_asleep(bar(L::LEMPTY + ls), ((tile / L::SST) & 1) ^ 1, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) break;
             if (lane == 0) mbar_arrive_expect_tx(bar(L::LFULL + ls), uint32_t(copies * box * 8));
             __syncwarp();
@@ -573,7 +602,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
                 bulk_load(sc, p.k_scale + row, uint32_t(box * 4), bar(L::LFULL + ls));
                 bulk_load(sc + 512, p.v_scale + row, uint32_t(box * 4), bar(L::LFULL + ls));
             }
-            ok = mbar_wait(bar(L::VEMPTY + vs), ((tile / L::VST) & 1) ^ 1, abort_flag);
+            ok = wait_asleep(bar(L::VEMPTY + vs), ((tile / L::VST) & 1) ^ 1, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) break;
             if (lane == 0) mbar_arrive_expect_tx(bar(L::VFULL + vs), uint32_t(copies * box * D));
             __syncwarp();
@@ -597,8 +626,8 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         bool any = false;
         int done[2] = {0, 0};  // P tiles consumed by each side
         auto pv = [&](int side, int tile) {
-            if (!mbar_wait(bar(L::PFULL + side), done[side] & 1, abort_flag)) return false;
-            if (!mbar_wait(bar(L::CFULL + tile % L::CST), (tile / L::CST) & 1, abort_flag)) return false;
+            if (!wait_asleep(bar(L::PFULL + side), done[side] & 1, abort_flag)) return false;
+            if (!wait_asleep(bar(L::CFULL + tile % L::CST), (tile / L::CST) & 1, abort_flag)) return false;
             tc_fence_after();
             const uint32_t v = sb + L::C_OFF + (tile % L::CST) * kTile * D * 2;
 #pragma unroll
@@ -610,13 +639,13 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             if (!both || side == 1) mma_commit(bar(L::CEMPTY + tile % L::CST));
             return true;
         };
-        bool ok = mbar_wait(bar(L::QFULL), 0, abort_flag);
+        bool ok = wait_asleep(bar(L::QFULL), 0, abort_flag);
         for (int j = 0; j < steps && ok; ++j) {
             const int side = j & 1, tile = both ? j >> 1 : j;
             if (j >= 2) ok = pv(side, both ? tile - 1 : tile - 2);
             if (!ok) break;
             const int ks = tile % L::KST;
-            ok = mbar_wait(bar(L::KFULL + ks), (tile / L::KST) & 1, abort_flag);
+            ok = wait_asleep(bar(L::KFULL + ks), (tile / L::KST) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
             const uint32_t kb = sb + L::K_OFF + ks * kTile * D, qb = sb + L::Q_OFF + side * 2 * L::QB;

@@ -906,15 +906,17 @@ int attend_splits(int64_t units, int64_t len) {
 }
 
 // Tall kernel, one CTA per SM: the number of slots whose whole waves of CTAs
-// take the fewest tile steps, counting what a CTA does besides (Q, the ends
-// of the pipeline, its partial output) as four.
-int attend_wide_splits(int64_t units, int64_t rows, int64_t len) {
+// take the fewest tile steps (1.2 us each), counting what a CTA does besides
+// (Q, the ends of the pipeline, its partial output: about 10 us) as eight,
+// and the writing and joining of one slot's outputs at 4 TB/s.
+int attend_wide_splits(int64_t units, int64_t rows, int64_t len, int64_t out_values) {
     const int64_t tiles = (len + attend::kTile - 1) / attend::kTile;
     const int64_t per_tile = rows > attend::kTile ? 2 : 1;
+    const int64_t slot_cost = out_values * 8 / 4800;  // thousandths of a step: 8 bytes a value at 4 TB/s, of 1.2 us
     int64_t best = 1, best_cost = INT64_MAX;
     for (int64_t s = 1; s <= 64 && s <= tiles; ++s) {
         const int64_t waves = (units * s + kAttendSms - 1) / kAttendSms;
-        const int64_t cost = waves * ((tiles + s - 1) / s * per_tile + 4);
+        const int64_t cost = waves * ((tiles + s - 1) / s * per_tile + 8) * 1000 + s * slot_cost;
         if (cost < best_cost) best = s, best_cost = cost;
     }
     return int(best);
@@ -937,7 +939,7 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t 
         a.wide_p = rows >= kWideFrom;
         const int64_t tile = a.wide_p ? attend::kWideRows : attend::kRows;
         a.tiles_p = (rows + tile - 1) / tile;
-        a.splits_p = a.wide_p ? attend_wide_splits(a.tiles_p * Hkv, rows, prefix_len)
+        a.splits_p = a.wide_p ? attend_wide_splits(a.tiles_p * Hkv, rows, prefix_len, T * Hq * D)
                               : attend_splits(a.tiles_p * Hkv, prefix_len);
     }
     if (max_pages > 0 || prefix_len == 0) {
@@ -945,7 +947,7 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t 
         a.wide_o = rows >= kWideFrom && max_pages > 0;
         const int64_t tile = a.wide_o ? attend::kWideRows : attend::kRows;
         a.tiles_o = (rows + tile - 1) / tile;
-        a.splits_o = a.wide_o ? attend_wide_splits(a.tiles_o * Hkv * B, rows, max_pages * page_size)
+        a.splits_o = a.wide_o ? attend_wide_splits(a.tiles_o * Hkv * B, rows, max_pages * page_size, T * Hq * D)
                               : attend_splits(a.tiles_o * Hkv * B, max_pages * page_size);
     }
     const int64_t slots = a.splits_p + a.splits_o;
