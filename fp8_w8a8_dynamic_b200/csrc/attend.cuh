@@ -558,26 +558,35 @@ join_kernel(const Params p) {
     float y[VPL], sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) y[j] = 0.0f;
+    constexpr int kAhead = 8;  // slots whose loads are in flight together
     for (int s0 = 0; s0 < slots; s0 += 32) {
         const int s = s0 + lane;
         const float w = s < slots ? ex2(p.part_lse[int64_t(s) * rows + row] - mz) : 0.0f;
         const int n = min(32, slots - s0);
-        for (int i = 0; i < n; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            if (wi > 0.0f) {
-                sum += wi;
-                const float* src = p.part + (int64_t(s0 + i) * rows + row) * D + lane * VPL;
-                if constexpr (VPL == 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(src);
-                    y[0] = fmaf(wi, v.x, y[0]);
-                    y[1] = fmaf(wi, v.y, y[1]);
-                    y[2] = fmaf(wi, v.z, y[2]);
-                    y[3] = fmaf(wi, v.w, y[3]);
-                } else {
-                    const float2 v = *reinterpret_cast<const float2*>(src);
-                    y[0] = fmaf(wi, v.x, y[0]);
-                    y[1] = fmaf(wi, v.y, y[1]);
+        for (int i0 = 0; i0 < n; i0 += kAhead) {
+            float wi[kAhead], v[kAhead][VPL];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                wi[i] = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
+                if (i0 + i >= n) wi[i] = 0.0f;
+                const float* src = p.part + (int64_t(s0 + i0 + i) * rows + row) * D + lane * VPL;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) v[i][j] = 0.0f;
+                if (wi[i] > 0.0f) {  // a slot without weight may hold anything
+                    if constexpr (VPL == 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(src);
+                        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+                    } else {
+                        const float2 x = *reinterpret_cast<const float2*>(src);
+                        v[i][0] = x.x, v[i][1] = x.y;
+                    }
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                sum += wi[i];
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) y[j] = fmaf(wi[i], v[i][j], y[j]);
             }
         }
     }

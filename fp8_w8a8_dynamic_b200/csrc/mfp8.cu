@@ -857,25 +857,26 @@ mfp8_status check_rope_args(const int32_t* pos, int n_axes, const uint8_t* axis,
 
 mfp8_status launch_rope(rope::Params p, int layout, cudaStream_t stream) {
     const int heads = p.nq + p.nk + p.nv;
-    const int lpr = p.vpr <= 2 ? 2 : p.vpr <= 4 ? 4 : p.vpr <= 8 ? 8 : p.vpr <= 16 ? 16 : 32;
-    // Whole tokens per block: enough of them to give every thread kItems
-    // vectors, but no more than leaves four blocks for each SM.
-    const int64_t per_block = int64_t(rope::kThreads) * rope::kItems / (int64_t(heads) * lpr);
-    int64_t tpb = per_block < rope::kMaxTokens ? per_block : rope::kMaxTokens;
-    const int64_t spread = p.T / (148 * 4);
-    if (tpb > spread) tpb = spread;
-    if (tpb < 1) tpb = 1;
-    p.tokens_per_block = int(tpb);
+    const int units = p.vpr / 2;
+    const int upr = units <= 1 ? 1 : units <= 2 ? 2 : units <= 4 ? 4 : units <= 8 ? 8 : 16;
+    // Threads per token: enough for a vector pair each, but at least a
+    // sixteenth of a block; all of a block while there are few tokens.
+    int shift = 7;  // kThreads
+    while (shift > 3 && (1 << (shift - 1)) >= upr && (1 << (shift - 1)) >= heads * upr &&
+           int64_t(p.T) >= int64_t(148) * 8 * (rope::kThreads >> (shift - 1)))
+        --shift;
+    p.tpt_shift = shift;
+    const int tpb = rope::kThreads >> shift;
     const dim3 grid(unsigned((p.T + tpb - 1) / tpb));
-    const int smem = int(tpb) * p.rot * int(sizeof(float));
+    const int smem = tpb * p.rot * int(sizeof(float));
     auto run = [&](auto kern) { return launch_pdl(kern, grid, rope::kThreads, stream, smem, p); };
     const bool il = layout == MFP8_ROPE_INTERLEAVED;
-    switch (lpr) {
+    switch (upr) {
+        case 1: return il ? run(rope::rope_store_kernel<1, true>) : run(rope::rope_store_kernel<1, false>);
         case 2: return il ? run(rope::rope_store_kernel<2, true>) : run(rope::rope_store_kernel<2, false>);
         case 4: return il ? run(rope::rope_store_kernel<4, true>) : run(rope::rope_store_kernel<4, false>);
         case 8: return il ? run(rope::rope_store_kernel<8, true>) : run(rope::rope_store_kernel<8, false>);
-        case 16: return il ? run(rope::rope_store_kernel<16, true>) : run(rope::rope_store_kernel<16, false>);
-        default: return il ? run(rope::rope_store_kernel<32, true>) : run(rope::rope_store_kernel<32, false>);
+        default: return il ? run(rope::rope_store_kernel<16, true>) : run(rope::rope_store_kernel<16, false>);
     }
 }
 
@@ -1517,10 +1518,10 @@ mfp8_status mfp8_kv_page_read(const void* pages, const float* scale, int64_t n_p
     if (st != MFP8_OK) return st;
     const int vpr = int(D / 8);
     const int lpr = vpr <= 2 ? 2 : vpr <= 4 ? 4 : vpr <= 8 ? 8 : vpr <= 16 ? 16 : 32;
-    const int64_t R = T * H, per_block = int64_t(rope::kThreads / lpr) * rope::kReadItems;
+    const int64_t R = T * H, per_block = int64_t(rope::kReadThreads / lpr) * rope::kReadItems;
     const dim3 grid(unsigned((R + per_block - 1) / per_block));
     auto run = [&](auto kern) {
-        return launch_pdl(kern, grid, rope::kThreads, static_cast<cudaStream_t>(stream), 0,
+        return launch_pdl(kern, grid, rope::kReadThreads, static_cast<cudaStream_t>(stream), 0,
                           static_cast<const uint2*>(pages), scale, slot, n_pages * page_size, page_shift(page_size),
                           int(R), int(H), vpr, static_cast<uint4*>(out_bf16));
     };

@@ -21,11 +21,15 @@
 // bytes are those of mfp8_kv_quantize on the rotated bf16 keys.  Token t goes
 // to slot[t] = page * page_size + place; a negative slot is padding.
 //
-// Memory-bound: every value is read once (16-byte vectors) and written once.
-// A block takes the rows of one or a few whole tokens, so the cosines and
-// sines of a token are computed once (64-bit sincos, about 40 operations per
-// pair) and shared through shared memory by all its heads; its rows' loads
-// are issued before that arithmetic.
+// Memory-bound: every value is read once (16-byte vectors) and written once,
+// so what counts is how few instructions a vector costs.  A thread takes two
+// vectors of a row at a time, in the half layout one of each half, which need
+// the same cosines and sines; those stay in its registers for all the heads
+// that it serves.  A block takes one token (or a few narrow ones): 64-bit
+// sincos, about 200 instructions for a pair, once per pair and token through
+// shared memory, behind the first loads.  Rotating 16384 tokens of 32 x 128
+// took 79 us with a vector per thread and shuffles between the halves (75% of
+// the issue slots busy); two vectors per thread: see kThreads.
 #pragma once
 
 #include <cstdint>
@@ -37,10 +41,8 @@
 namespace mfp8 {
 namespace rope {
 
-constexpr int kThreads = 256;
-constexpr int kItems = 3;       // row vectors per thread and pass, loads issued first
-constexpr int kMaxTokens = 16;  // tokens per block
-constexpr int kMaxHalf = 128;   // rot / 2 <= D / 2 <= 128
+constexpr int kThreads = 128;
+constexpr int kItems = 3;       // vector pairs per thread and pass, loads issued first
 
 // Rows of a token, in order: nq rotated rows written to Y, nk rotated rows
 // quantized into the K pages, nv rows quantized into the V pages.  rot = 0
@@ -56,7 +58,7 @@ struct Params {
     double mscale;
     int T, nq, nk, nv;
     int vpr;  // vectors per row, D / 8
-    int tokens_per_block;
+    int tpt_shift;  // log2 of the threads per token
     uint4* Y;
     int64_t ldy;
     const int64_t* slot;
@@ -87,118 +89,138 @@ __device__ __forceinline__ void cos_sin(int32_t pos, float inv_freq, double msca
     s = float(sd * mscale);
 }
 
-// Two values of a row and their partners' (half layout): fl(x c) + fl(p s),
-// the sign of s chosen by the caller.
-__device__ __forceinline__ uint32_t rotate2(uint32_t x, uint32_t p, float c0, float c1, float s0, float s1) {
-    const uint64_t a = mul2(pack2(bf16_lo(x), bf16_hi(x)), pack2(c0, c1));
-    const uint64_t b = mul2(pack2(bf16_lo(p), bf16_hi(p)), pack2(s0, s1));
+// Half layout: two pairs, x1 and x2 packed bf16 words.
+__device__ __forceinline__ void rotate_half2(uint32_t& x1, uint32_t& x2, float c0, float c1, float s0, float s1) {
+    const uint64_t a = pack2(bf16_lo(x1), bf16_hi(x1)), b = pack2(bf16_lo(x2), bf16_hi(x2));
+    const uint64_t c = pack2(c0, c1), s = pack2(s0, s1);
     float lo, hi;
-    unpack2(add2(a, b), lo, hi);
-    const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&y);
+    unpack2(sub2(mul2(a, c), mul2(b, s)), lo, hi);
+    const __nv_bfloat162 y1 = __floats2bfloat162_rn(lo, hi);
+    unpack2(add2(mul2(b, c), mul2(a, s)), lo, hi);
+    const __nv_bfloat162 y2 = __floats2bfloat162_rn(lo, hi);
+    x1 = *reinterpret_cast<const uint32_t*>(&y1);
+    x2 = *reinterpret_cast<const uint32_t*>(&y2);
 }
 
-// LPR lanes per row, a power of two >= D / 8.
-template <int LPR, bool INTERLEAVED>
+// Interleaved layout: one pair, a packed bf16 word.
+__device__ __forceinline__ void rotate_word(uint32_t& x, float c, float s) {
+    const float a = bf16_lo(x), b = bf16_hi(x);
+    float lo, hi;
+    unpack2(add2(mul2(pack2(a, b), pack2(c, c)), mul2(pack2(b, a), pack2(-s, s))), lo, hi);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
+    x = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// UPR lanes per row, a power of two >= D / 16, two vectors each.
+template <int UPR, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads)
 rope_store_kernel(const Params p) {
     grid_launch_dependents();
     grid_dependency_wait();  // X may be the previous kernel's output
-    extern __shared__ __align__(16) float cs[];  // cosines, then sines, [tokens_per_block][rot / 2]
+    extern __shared__ __align__(16) float cs[];  // cosines, then sines, [tokens of the block][rot / 2]
     const int half = p.rot >> 1;
-    const int tok0 = blockIdx.x * p.tokens_per_block;
-    const int toks = min(p.tokens_per_block, p.T - tok0);
+    const int tpt = 1 << p.tpt_shift;
+    const int tpb = kThreads >> p.tpt_shift;
+    const int tok0 = blockIdx.x * tpb;
+    const int tb = int(threadIdx.x) >> p.tpt_shift;  // token within the block
+    const int token = tok0 + tb;
+    const int j = int(threadIdx.x) & (tpt - 1);
+    const int u = j % UPR, h0 = j / UPR, hstep = tpt / UPR;
     const int heads = p.nq + p.nk + p.nv;
-    const int rows = toks * heads;
-    const int v = threadIdx.x % LPR;
-    const int lane = threadIdx.x & 31;
-    constexpr int kRowsPerPass = kThreads / LPR;
-    float* cosv = cs;
-    float* sinv = cs + p.tokens_per_block * half;
+    // the two vectors of a row: the same places in both halves, or neighbours
+    const int hv = p.rot >> 4;
+    const bool turns = u < hv;  // (interleaved: vectors 2u and 2u + 1 lie below rot together)
+    const int v0 = INTERLEAVED || half == 0 ? 2 * u : turns ? u : hv + u + (u - hv);
+    const int v1 = INTERLEAVED || !turns ? v0 + 1 : v0 + hv;
+    const bool live = token < p.T && u < (p.vpr >> 1);
+    const uint4* x = p.X + int64_t(token) * p.ldx;
 
-    for (int base = 0; base < rows; base += kRowsPerPass * kItems) {
-        uint4 x[kItems];
+    uint4 a[kItems], b[kItems];
+    auto load = [&](int base) {
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            const int row = base + k * kRowsPerPass + int(threadIdx.x) / LPR;
-            x[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < rows && v < p.vpr) {
-                const int t = row / heads;
-                x[k] = p.X[int64_t(tok0 + t) * p.ldx + int64_t(row - t * heads) * p.vpr + v];
+            const int h = base + k * hstep;
+            a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (live && h < heads) {
+                a[k] = x[int64_t(h) * p.vpr + v0];
+                b[k] = x[int64_t(h) * p.vpr + v1];
             }
         }
-        if (base == 0 && half > 0) {
-            for (int i = threadIdx.x; i < toks * half; i += kThreads) {
-                const int t = i / half, f = i - t * half;
-                const int ax = p.axis != nullptr ? min(int(p.axis[f]), p.n_axes - 1) : 0;
-                cos_sin(p.pos[int64_t(ax) * p.T + tok0 + t], p.inv_freq[f], p.mscale, cosv[i], sinv[i]);
-            }
-            __syncthreads();
+    };
+    load(h0);
+    float c[8], s[8];
+    if (half > 0) {
+        float* cosv = cs;
+        float* sinv = cs + tpb * half;
+        const int n = min(tpb, p.T - tok0) * half;
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const int t = i / half, f = i - t * half;
+            const int ax = p.axis != nullptr ? min(int(p.axis[f]), p.n_axes - 1) : 0;
+            cos_sin(p.pos[int64_t(ax) * p.T + tok0 + t], p.inv_freq[f], p.mscale, cosv[i], sinv[i]);
         }
+        __syncthreads();
+        if (live && turns) {
+#pragma unroll
+            for (int q = 0; q < 8; q += 4) {
+                const float4 cv = *reinterpret_cast<const float4*>(cosv + tb * half + u * 8 + q);
+                const float4 sv = *reinterpret_cast<const float4*>(sinv + tb * half + u * 8 + q);
+                c[q] = cv.x, c[q + 1] = cv.y, c[q + 2] = cv.z, c[q + 3] = cv.w;
+                s[q] = sv.x, s[q + 1] = sv.y, s[q + 2] = sv.z, s[q + 3] = sv.w;
+            }
+        }
+    }
+    // where the token's rows go in the pages
+    int64_t place = -1;  // row within its page
+    int64_t page = 0;
+    if (p.nk + p.nv > 0 && token < p.T) {
+        const int64_t slot = p.slot[token];
+        if (slot >= p.n_slots) record_device_status(MFP8_ERR_INDEX);
+        else if (slot >= 0) {
+            page = slot >> p.ps_shift;
+            place = slot & ((int64_t(1) << p.ps_shift) - 1);
+        }
+    }
+    // every thread of a warp makes the same number of passes (the shuffles want them all)
+    for (int base = h0; base - h0 < heads; base += kItems * hstep) {
+        if (base != h0) load(base);
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            const int row = base + k * kRowsPerPass + int(threadIdx.x) / LPR;
-            const bool live = row < rows && v < p.vpr;
-            const int t = row < rows ? row / heads : 0;
-            const int h = row < rows ? row - t * heads : 0;
-            uint4 y = x[k];
-            if (half > 0) {
-                if (INTERLEAVED) {
-                    if (live && h < p.nq + p.nk && v * 8 < p.rot) {
-                        const float4 c = *reinterpret_cast<const float4*>(cosv + t * half + v * 4);
-                        const float4 s = *reinterpret_cast<const float4*>(sinv + t * half + v * 4);
-                        // the pair is one word: (x1, x2) and its swap (x2, x1)
-                        y.x = rotate2(x[k].x, __byte_perm(x[k].x, 0u, 0x1032u), c.x, c.x, -s.x, s.x);
-                        y.y = rotate2(x[k].y, __byte_perm(x[k].y, 0u, 0x1032u), c.y, c.y, -s.y, s.y);
-                        y.z = rotate2(x[k].z, __byte_perm(x[k].z, 0u, 0x1032u), c.z, c.z, -s.z, s.z);
-                        y.w = rotate2(x[k].w, __byte_perm(x[k].w, 0u, 0x1032u), c.w, c.w, -s.w, s.w);
-                    }
-                } else {
-                    const int hv = p.rot >> 4;  // vectors in each half
-                    const bool first = v < hv;
-                    const int src = (lane & ~(LPR - 1)) + (first ? v + hv : v < 2 * hv ? v - hv : v);
-                    uint4 q;
-                    q.x = __shfl_sync(0xffffffffu, x[k].x, src);
-                    q.y = __shfl_sync(0xffffffffu, x[k].y, src);
-                    q.z = __shfl_sync(0xffffffffu, x[k].z, src);
-                    q.w = __shfl_sync(0xffffffffu, x[k].w, src);
-                    if (live && h < p.nq + p.nk && v < 2 * hv) {
-                        const int f = t * half + (first ? v : v - hv) * 8;
-                        const float4 c0 = *reinterpret_cast<const float4*>(cosv + f);
-                        const float4 c1 = *reinterpret_cast<const float4*>(cosv + f + 4);
-                        float4 s0 = *reinterpret_cast<const float4*>(sinv + f);
-                        float4 s1 = *reinterpret_cast<const float4*>(sinv + f + 4);
-                        if (first) {
-                            s0 = make_float4(-s0.x, -s0.y, -s0.z, -s0.w);
-                            s1 = make_float4(-s1.x, -s1.y, -s1.z, -s1.w);
-                        }
-                        y.x = rotate2(x[k].x, q.x, c0.x, c0.y, s0.x, s0.y);
-                        y.y = rotate2(x[k].y, q.y, c0.z, c0.w, s0.z, s0.w);
-                        y.z = rotate2(x[k].z, q.z, c1.x, c1.y, s1.x, s1.y);
-                        y.w = rotate2(x[k].w, q.w, c1.z, c1.w, s1.z, s1.w);
+            const int h = base + k * hstep;
+            if (h - h0 >= heads) break;  // no thread has a row here
+            const bool mine = live && h < heads;
+            if (half > 0 && turns && h < p.nq + p.nk) {
+                uint32_t* xa = reinterpret_cast<uint32_t*>(&a[k]);
+                uint32_t* xb = reinterpret_cast<uint32_t*>(&b[k]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (INTERLEAVED) {
+                        rotate_word(xa[q], c[q], s[q]);
+                        rotate_word(xb[q], c[q + 4], s[q + 4]);
+                    } else {
+                        rotate_half2(xa[q], xb[q], c[2 * q], c[2 * q + 1], s[2 * q], s[2 * q + 1]);
                     }
                 }
             }
-            if (live && h < p.nq) p.Y[int64_t(tok0 + t) * p.ldy + int64_t(h) * p.vpr + v] = y;
+            if (mine && h < p.nq) {
+                uint4* y = p.Y + int64_t(token) * p.ldy + int64_t(h) * p.vpr;
+                y[v0] = a[k];
+                y[v1] = b[k];
+            }
             if (p.nk + p.nv > 0) {
-                const uint32_t acc = absmax_bits_u4(y, 0u);
+                const uint32_t acc = absmax_bits_u4(b[k], absmax_bits_u4(a[k], 0u));
                 uint32_t amax = max(acc & 0xffffu, acc >> 16);
 #pragma unroll
-                for (int off = 1; off < LPR; off <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-                if (live && h >= p.nq) {
-                    const int64_t slot = p.slot[tok0 + t];
-                    if (slot >= p.n_slots) {
-                        record_device_status(MFP8_ERR_INDEX);
-                    } else if (slot >= 0) {
-                        const bool key = h < p.nq + p.nk;
-                        const int hk = key ? h - p.nq : h - p.nq - p.nk;
-                        const int nh = key ? p.nk : p.nv;
-                        const int64_t r = ((((slot >> p.ps_shift) * nh) + hk) << p.ps_shift) +
-                                          (slot & ((int64_t(1) << p.ps_shift) - 1));
-                        const float s = scale_from_absmax_bits(amax);
-                        if (v == 0) (key ? p.k_scale : p.v_scale)[r] = s;
-                        (key ? p.K : p.V)[r * p.vpr + v] = quantize8(y, s, __frcp_rn(s));
-                    }
+                for (int off = 1; off < UPR; off <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+                if (mine && h >= p.nq && place >= 0) {
+                    const bool key = h < p.nq + p.nk;
+                    const int hk = key ? h - p.nq : h - p.nq - p.nk;
+                    const int64_t r = ((page * (key ? p.nk : p.nv) + hk) << p.ps_shift) + place;
+                    const float sc = scale_from_absmax_bits(amax);
+                    const float rc = __frcp_rn(sc);
+                    if (u == 0) (key ? p.k_scale : p.v_scale)[r] = sc;
+                    uint2* q = (key ? p.K : p.V) + r * p.vpr;
+                    q[v0] = quantize8(a[k], sc, rc);
+                    q[v1] = quantize8(b[k], sc, rc);
                 }
             }
         }
@@ -210,14 +232,15 @@ rope_store_kernel(const Params p) {
 // kReadItems vectors of 8 codes, all loads issued first; a row's lanes are
 // contiguous.
 constexpr int kReadItems = 4;
+constexpr int kReadThreads = 256;
 
 template <int LPR>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kReadThreads)
 page_read_kernel(const uint2* __restrict__ C, const float* __restrict__ S, const int64_t* __restrict__ slot,
                  int64_t n_slots, int ps_shift, int R, int H, int vpr, uint4* __restrict__ out) {
     grid_launch_dependents();
     grid_dependency_wait();
-    constexpr int kRowsPerPass = kThreads / LPR;
+    constexpr int kRowsPerPass = kReadThreads / LPR;
     const int v = threadIdx.x % LPR;
     const int64_t row0 = int64_t(blockIdx.x) * (kRowsPerPass * kReadItems) + threadIdx.x / LPR;
     uint2 q[kReadItems];

@@ -7,6 +7,7 @@ every step of the computation runs in the CUDA kernels of libmfp8.so.  There
 is no CPU fallback: without the built library every call raises.
 """
 import ctypes
+import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -441,36 +442,34 @@ class Kv8Cache:
         return kv8_read(self.codes[:tq], self.scale[:tq // 64], self.zero[:tq // 64], self.tail, out=out)
 
 
-class _On:
-    """Where a helper's kernels run: on `stream` (or torch's current one) of
-    the current device, which must hold every tensor.  With a stream other
-    than the current one, outputs are allocated on it and inputs are marked
-    as used by it, so torch's allocator does not hand their memory on early."""
-
-    def __init__(self, where, stream, tensors):
-        import torch
-        dev = torch.cuda.current_device()
+def _on(where, stream, tensors):
+    """The stream handle that a helper's kernels run on: `stream`, or torch's
+    current one, of the current device, which must hold every tensor (a
+    tensor elsewhere answers another device number, or -1)."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{where}: tensors must be on the current CUDA device ({dev})")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"{where}: the stream belongs to another device")
+    if stream.cuda_stream != torch._C._cuda_getCurrentRawStream(dev):
+        # torch's allocator must not hand these on before the kernels are done with them
         for t in tensors:
-            if t is not None and (not t.is_cuda or t.get_device() != dev):
-                raise ValueError(f"{where}: tensors must be on the current CUDA device ({dev})")
-        cur = torch.cuda.current_stream()
-        self.device = cur.device
-        self.other = None
-        if stream is not None and stream.cuda_stream != cur.cuda_stream:
-            if stream.device_index != dev:
-                raise ValueError(f"{where}: the stream belongs to another device")
-            self.other = stream
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-        self.handle = (stream or cur).cuda_stream
+            if t is not None:
+                t.record_stream(stream)
+    return stream.cuda_stream
 
-    def empty(self, shape, dtype):
-        import torch
-        if self.other is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.other):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+
+def _new(like, shape, dtype, stream):
+    """An uninitialised tensor on like's device, allocated on the stream that writes it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _need(ok, where, what):
@@ -479,43 +478,51 @@ def _need(ok, where, what):
 
 
 def _rows(where, x, name="x"):
-    """bf16 [T, H, D] with whole head rows one after the other; elements between tokens."""
+    """bf16 [T, H, D] with whole head rows one after the other: T, H, D, elements between tokens."""
     import torch
-    _need(x.dim() == 3 and x.dtype == torch.bfloat16, where, f"{name} must be bf16 [T, H, D]")
+    if x.dtype is not torch.bfloat16 or x.dim() != 3:
+        raise ValueError(f"{where}: {name} must be bf16 [T, H, D]")
     T, H, D = x.shape
-    _need(T == 0 or ((D < 2 or x.stride(2) == 1) and (H < 2 or x.stride(1) == D)), where,
-          f"the head rows of a token in {name} must be contiguous")
-    return T, H, D, x.stride(0) if T > 1 else H * D
+    if x.is_contiguous():
+        return T, H, D, H * D
+    ld, sh, sd = x.stride()
+    if T and ((D > 1 and sd != 1) or (H > 1 and sh != D)):
+        raise ValueError(f"{where}: the head rows of a token in {name} must be contiguous")
+    return T, H, D, ld if T > 1 else H * D
 
 
 def _rope_args(where, T, pos, inv_freq, axis):
     """(n_axes, rot) of position and frequency tensors that fit."""
     import torch
-    _need(pos.dtype == torch.int32 and pos.dim() in (1, 2) and pos.shape[-1] == T and pos.is_contiguous(), where,
-          "pos must be contiguous int32 [T] or [axes, T]")
-    _need(inv_freq.dtype == torch.float32 and inv_freq.dim() == 1 and inv_freq.is_contiguous(), where,
-          "inv_freq must be contiguous fp32 [rot / 2]")
+    if pos.dtype is not torch.int32 or pos.dim() not in (1, 2) or pos.shape[-1] != T or not pos.is_contiguous():
+        raise ValueError(f"{where}: pos must be contiguous int32 [T] or [axes, T]")
+    if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError(f"{where}: inv_freq must be contiguous fp32 [rot / 2]")
     n_axes = pos.shape[0] if pos.dim() == 2 else 1
-    _need(n_axes == 1 or axis is not None, where, "several position axes need `axis`")
-    _need(axis is None or (axis.dtype == torch.uint8 and axis.shape == inv_freq.shape and axis.is_contiguous()),
-          where, "axis must be contiguous uint8 [rot / 2]")
-    return n_axes, 2 * inv_freq.numel()
+    if axis is None:
+        _need(n_axes == 1, where, "several position axes need `axis`")
+    else:
+        _need(axis.dtype is torch.uint8 and axis.shape == inv_freq.shape and axis.is_contiguous(), where,
+              "axis must be contiguous uint8 [rot / 2]")
+    return n_axes, 2 * inv_freq.shape[0]
 
 
-def _pool(where, pages, scale, H, D):
-    """(n_pages, page_size) of a paged cache tensor and its scales."""
+def _pool(where, pages, scale):
+    """(n_pages, H, page_size, D) of a paged cache tensor with its scales."""
     import torch
-    _need(pages.dtype == torch.uint8 and pages.dim() == 4 and pages.is_contiguous() and pages.shape[1] == H
-          and pages.shape[3] == D, where, f"pages must be contiguous uint8 [n_pages, {H}, page_size, {D}]")
-    _need(scale.dtype == torch.float32 and scale.shape == pages.shape[:3] and scale.is_contiguous(), where,
-          "scale must be contiguous fp32 [n_pages, H, page_size]")
-    return pages.shape[0], pages.shape[2]
+    shape = pages.shape
+    if pages.dtype is not torch.uint8 or len(shape) != 4 or not pages.is_contiguous():
+        raise ValueError(f"{where}: pages must be contiguous uint8 [n_pages, H, page_size, D]")
+    if scale.dtype is not torch.float32 or scale.shape != shape[:3] or not scale.is_contiguous():
+        raise ValueError(f"{where}: scale must be contiguous fp32 [n_pages, H, page_size]")
+    return shape
 
 
-def _slots(where, slot, T=None):
+def _slots(where, slot):
     import torch
-    _need(slot.dtype == torch.int64 and slot.dim() == 1 and slot.is_contiguous() and (T is None or len(slot) == T),
-          where, "slot must be contiguous int64 [T]")
+    if slot.dtype is not torch.int64 or slot.dim() != 1 or not slot.is_contiguous():
+        raise ValueError(f"{where}: slot must be contiguous int64 [T]")
+    return slot.shape[0]
 
 
 def rope_frequencies(rot, theta, scaling=ROPE_SCALE_NONE, factor=1.0, trained_len=0, beta_fast=32.0, beta_slow=1.0,
@@ -534,16 +541,16 @@ def rope(x, pos, inv_freq, axis=None, layout=ROPE_HALF, mscale=1.0, out=None, st
     columns of a packed projection) -> rotated bf16 [T, H, D].  pos int32 [T]
     or [axes, T]; inv_freq fp32 [rot / 2]; axis uint8 [rot / 2].  `out` may
     be x itself."""
-    import torch
     T, H, D, ldx = _rows("rope", x)
     n_axes, rot = _rope_args("rope", T, pos, inv_freq, axis)
-    on = _On("rope", stream, (x, pos, inv_freq, axis, out))
+    handle = _on("rope", stream, (x, pos, inv_freq, axis, out))
     if out is None:
-        out = on.empty((T, H, D), torch.bfloat16)
-    _need(out.shape == x.shape, "rope", "out must have x's shape")
-    ldy = _rows("rope", out, "out")[3]
-    _check(mfp8_rope(x.data_ptr(), ldx, T, H, D, pos.data_ptr(), n_axes, _ptr(axis), inv_freq.data_ptr(), rot, layout,
-                     mscale, out.data_ptr(), ldy, on.handle), "mfp8_rope")
+        out, ldy = _new(x, (T, H, D), x.dtype, stream), H * D
+    else:
+        _need(out.shape == x.shape, "rope", "out must have x's shape")
+        ldy = _rows("rope", out, "out")[3]
+    _check(lib().mfp8_rope(x.data_ptr(), ldx, T, H, D, pos.data_ptr(), n_axes, _ptr(axis), inv_freq.data_ptr(), rot,
+                           layout, mscale, out.data_ptr(), ldy, handle), "mfp8_rope")
     return out
 
 
@@ -551,29 +558,30 @@ def kv_page_store(kv, slot, pages, scale, stream=None):
     """Quantize kv bf16 [T, H, D] (tokens may be strided) into the slots (int64
     [T], negative: skipped) of pages uint8 [n_pages, H, page_size, D] and
     scale fp32 [n_pages, H, page_size]."""
-    T, H, D, ld = _rows("kv_page_store", kv, "kv")
-    n_pages, ps = _pool("kv_page_store", pages, scale, H, D)
-    _slots("kv_page_store", slot, T)
-    on = _On("kv_page_store", stream, (kv, slot, pages, scale))
-    _check(mfp8_kv_page_store(kv.data_ptr(), ld, slot.data_ptr(), T, H, D, pages.data_ptr(), scale.data_ptr(), n_pages,
-                              ps, on.handle), "mfp8_kv_page_store")
+    w = "kv_page_store"
+    T, H, D, ld = _rows(w, kv, "kv")
+    n_pages, hp, ps, dp = _pool(w, pages, scale)
+    _need((hp, dp) == (H, D), w, "kv and pages must have the same heads and head size")
+    _need(_slots(w, slot) == T, w, "slot must have one entry per token")
+    handle = _on(w, stream, (kv, slot, pages, scale))
+    _check(lib().mfp8_kv_page_store(kv.data_ptr(), ld, slot.data_ptr(), T, H, D, pages.data_ptr(), scale.data_ptr(),
+                                    n_pages, ps, handle), "mfp8_kv_page_store")
 
 
 def kv_page_read(pages, scale, slot, out=None, stream=None):
     """The rows in slot int64 [T] of a paged cache as bf16 [T, H, D] (zeros for a negative slot)."""
     import torch
-    _need(pages.dim() == 4, "kv_page_read", "pages must be uint8 [n_pages, H, page_size, D]")
-    H, D = pages.shape[1], pages.shape[3]
-    n_pages, ps = _pool("kv_page_read", pages, scale, H, D)
-    _slots("kv_page_read", slot)
-    T = slot.shape[0]
-    on = _On("kv_page_read", stream, (pages, scale, slot, out))
+    w = "kv_page_read"
+    n_pages, H, ps, D = _pool(w, pages, scale)
+    T = _slots(w, slot)
+    handle = _on(w, stream, (pages, scale, slot, out))
     if out is None:
-        out = on.empty((T, H, D), torch.bfloat16)
-    _need(out.dtype == torch.bfloat16 and out.shape == (T, H, D) and out.is_contiguous(), "kv_page_read",
-          "out must be contiguous bf16 [T, H, D]")
-    _check(mfp8_kv_page_read(pages.data_ptr(), scale.data_ptr(), n_pages, ps, slot.data_ptr(), T, H, D, out.data_ptr(),
-                             on.handle), "mfp8_kv_page_read")
+        out = _new(pages, (T, H, D), torch.bfloat16, stream)
+    else:
+        _need(out.dtype is torch.bfloat16 and out.shape == (T, H, D) and out.is_contiguous(), w,
+              "out must be contiguous bf16 [T, H, D]")
+    _check(lib().mfp8_kv_page_read(pages.data_ptr(), scale.data_ptr(), n_pages, ps, slot.data_ptr(), T, H, D,
+                                   out.data_ptr(), handle), "mfp8_kv_page_read")
     return out
 
 
@@ -585,25 +593,31 @@ def rope_kv_store(qkv, n_heads, pos, inv_freq, slot, k_pages, k_scale, v_pages, 
     those of the pages."""
     import torch
     w = "rope_kv_store"
-    _need(k_pages.dim() == 4, w, "pages must be uint8 [n_pages, H, page_size, D]")
-    Hkv, D = k_pages.shape[1], k_pages.shape[3]
-    n_pages, ps = _pool(w, k_pages, k_scale, Hkv, D)
-    _need(_pool(w, v_pages, v_scale, Hkv, D) == (n_pages, ps), w, "k_pages and v_pages must have one shape")
-    _need(qkv.dim() == 2 and qkv.dtype == torch.bfloat16 and qkv.shape[1] == (n_heads + 2 * Hkv) * D
-          and (qkv.shape[0] == 0 or qkv.stride(1) == 1), w, "qkv must be bf16 [T, (n_heads + 2 Hkv) D]")
+    shape = _pool(w, k_pages, k_scale)
+    _need(_pool(w, v_pages, v_scale) == shape, w, "k_pages and v_pages must have one shape")
+    n_pages, Hkv, ps, D = shape
+    if qkv.dtype is not torch.bfloat16 or qkv.dim() != 2 or qkv.shape[1] != (n_heads + 2 * Hkv) * D or (
+            qkv.shape[0] and qkv.stride(1) != 1):
+        raise ValueError(f"{w}: qkv must be bf16 [T, (n_heads + 2 Hkv) D]")
     T = qkv.shape[0]
     n_axes, rot = _rope_args(w, T, pos, inv_freq, axis)
-    _slots(w, slot, T)
-    on = _On(w, stream, (qkv, pos, inv_freq, axis, slot, k_pages, k_scale, v_pages, v_scale, out))
+    _need(_slots(w, slot) == T, w, "slot must have one entry per token")
+    handle = _on(w, stream, (qkv, pos, inv_freq, axis, slot, k_pages, k_scale, v_pages, v_scale, out))
     if out is None:
-        out = on.empty((T, n_heads, D), torch.bfloat16)
-    _need(out.dtype == torch.bfloat16 and out.shape == (T, n_heads, D) and out.is_contiguous(), w,
-          "out must be contiguous bf16 [T, n_heads, D]")
-    _check(mfp8_rope_kv_store(qkv.data_ptr(), qkv.stride(0) if T > 1 else qkv.shape[1], T, n_heads, Hkv, D,
-                              pos.data_ptr(), n_axes, _ptr(axis), inv_freq.data_ptr(), rot, layout, mscale,
-                              slot.data_ptr(), out.data_ptr(), k_pages.data_ptr(), k_scale.data_ptr(),
-                              v_pages.data_ptr(), v_scale.data_ptr(), n_pages, ps, on.handle), "mfp8_rope_kv_store")
+        out = _new(qkv, (T, n_heads, D), qkv.dtype, stream)
+    else:
+        _need(out.dtype is torch.bfloat16 and out.shape == (T, n_heads, D) and out.is_contiguous(), w,
+              "out must be contiguous bf16 [T, n_heads, D]")
+    _check(lib().mfp8_rope_kv_store(qkv.data_ptr(), qkv.stride(0) if T > 1 else qkv.shape[1], T, n_heads, Hkv, D,
+                                    pos.data_ptr(), n_axes, _ptr(axis), inv_freq.data_ptr(), rot, layout, mscale,
+                                    slot.data_ptr(), out.data_ptr(), k_pages.data_ptr(), k_scale.data_ptr(),
+                                    v_pages.data_ptr(), v_scale.data_ptr(), n_pages, ps, handle), "mfp8_rope_kv_store")
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace(*sizes):
+    return mfp8_prefix_attention_workspace_bytes(*sizes)
 
 
 def prefix_attention(q, q_start, kv_len, page_table, prefix_pages, prefix_len, k_pages, k_scale, v_pages, v_scale,
@@ -612,51 +626,54 @@ def prefix_attention(q, q_start, kv_len, page_table, prefix_pages, prefix_len, k
     q bf16 [T, Hq, D] (tokens may be strided); q_start int32 [B + 1]: sequence
     b has the query tokens q_start[b] .. q_start[b + 1] - 1, at most max_q;
     kv_len int32 [B]: its own cached tokens, the query tokens the last of them;
-    page_table int32 [B, max_pages] (a row may be strided) or None;
+    page_table int32 [B, max_pages] (rows may be strided) or None;
     prefix_pages int32 [>= ceil(prefix_len / page_size)] or None, prefix_len
     an int; scale defaults to D ** -0.5.  -> bf16 [T, Hq, D], with want_lse
     also the natural log-sum-exp fp32 [T, Hq]."""
     import torch
     w = "prefix_attention"
-    T, Hq, D, ldq = _rows(w, q, "q")
-    _need(k_pages.dim() == 4, w, "pages must be uint8 [n_pages, H, page_size, D]")
-    Hkv = k_pages.shape[1]
-    n_pages, ps = _pool(w, k_pages, k_scale, Hkv, D)
-    _need(_pool(w, v_pages, v_scale, Hkv, D) == (n_pages, ps), w, "k_pages and v_pages must have one shape")
     i32 = torch.int32
-    _need(kv_len.dtype == i32 and kv_len.dim() == 1 and kv_len.is_contiguous(), w, "kv_len must be contiguous int32 [B]")
+    T, Hq, D, ldq = _rows(w, q, "q")
+    shape = _pool(w, k_pages, k_scale)
+    _need(_pool(w, v_pages, v_scale) == shape, w, "k_pages and v_pages must have one shape")
+    n_pages, Hkv, ps, dp = shape
+    _need(dp == D, w, "q and the pages must have one head size")
+    if kv_len.dtype is not i32 or kv_len.dim() != 1 or not kv_len.is_contiguous():
+        raise ValueError(f"{w}: kv_len must be contiguous int32 [B]")
     B = kv_len.shape[0]
-    _need(q_start.dtype == i32 and q_start.shape == (B + 1,) and q_start.is_contiguous(), w,
-          "q_start must be contiguous int32 [B + 1]")
+    if q_start.dtype is not i32 or q_start.shape != (B + 1,) or not q_start.is_contiguous():
+        raise ValueError(f"{w}: q_start must be contiguous int32 [B + 1]")
     max_pages = ld = 0
     if page_table is not None:
-        _need(page_table.dtype == i32 and page_table.dim() == 2 and page_table.shape[0] == B, w,
-              "page_table must be int32 [B, max_pages]")
+        if page_table.dtype is not i32 or page_table.dim() != 2 or page_table.shape[0] != B:
+            raise ValueError(f"{w}: page_table must be int32 [B, max_pages]")
         max_pages = page_table.shape[1]
         _need(max_pages < 2 or page_table.stride(1) == 1, w, "the rows of page_table must be contiguous")
         ld = page_table.stride(0) if B > 1 else max_pages
     if prefix_len:
-        _need(prefix_pages is not None and prefix_pages.dtype == i32 and prefix_pages.dim() == 1
+        _need(prefix_pages is not None and prefix_pages.dtype is i32 and prefix_pages.dim() == 1
               and prefix_pages.is_contiguous() and 0 < prefix_len <= prefix_pages.shape[0] * ps, w,
               "prefix_pages must be contiguous int32 and cover prefix_len")
-    on = _On(w, stream, (q, q_start, kv_len, page_table, prefix_pages, k_pages, k_scale, v_pages, v_scale, out,
-                         workspace))
+    handle = _on(w, stream, (q, q_start, kv_len, page_table, prefix_pages, k_pages, k_scale, v_pages, v_scale, out,
+                             workspace))
     if out is None:
-        out = on.empty((T, Hq, D), torch.bfloat16)
-    _need(out.dtype == torch.bfloat16 and out.shape == (T, Hq, D) and out.is_contiguous(), w,
-          "out must be contiguous bf16 [T, Hq, D]")
-    lse = on.empty((T, Hq), torch.float32) if want_lse else None
+        out = _new(q, (T, Hq, D), q.dtype, stream)
+    else:
+        _need(out.dtype is torch.bfloat16 and out.shape == (T, Hq, D) and out.is_contiguous(), w,
+              "out must be contiguous bf16 [T, Hq, D]")
+    lse = _new(q, (T, Hq), torch.float32, stream) if want_lse else None
     if workspace is None:
-        nbytes = mfp8_prefix_attention_workspace_bytes(T, B, max_q, Hq, Hkv, D, prefix_len, max_pages, ps)
-        workspace = on.empty((nbytes,), torch.uint8) if nbytes else None
+        nbytes = _attention_workspace(T, B, max_q, Hq, Hkv, D, prefix_len, max_pages, ps)
+        if nbytes:
+            workspace = _new(q, (nbytes,), torch.uint8, stream)
     else:
         _need(workspace.is_contiguous(), w, "workspace must be contiguous")
-    _check(mfp8_prefix_attention(
+        nbytes = workspace.nbytes
+    _check(lib().mfp8_prefix_attention(
         q.data_ptr(), ldq, T, Hq, Hkv, D, q_start.data_ptr(), kv_len.data_ptr(), B, max_q, k_pages.data_ptr(),
         k_scale.data_ptr(), v_pages.data_ptr(), v_scale.data_ptr(), n_pages, ps, _ptr(prefix_pages), prefix_len,
-        _ptr(page_table) if max_pages else None, ld, max_pages, scale if scale is not None else D ** -0.5,
-        out.data_ptr(), _ptr(lse), _ptr(workspace), workspace.nbytes if workspace is not None else 0, on.handle),
-        "mfp8_prefix_attention")
+        page_table.data_ptr() if max_pages else None, ld, max_pages, scale if scale is not None else D ** -0.5,
+        out.data_ptr(), _ptr(lse), _ptr(workspace), nbytes, handle), "mfp8_prefix_attention")
     return (out, lse) if want_lse else out
 
 
