@@ -28,8 +28,10 @@
 // that it serves.  A block takes one token (or a few narrow ones): 64-bit
 // sincos, about 200 instructions for a pair, once per pair and token through
 // shared memory, behind the first loads.  Rotating 16384 tokens of 32 x 128
-// took 79 us with a vector per thread and shuffles between the halves (75% of
-// the issue slots busy); two vectors per thread: see kThreads.
+// values (268 MB) took 79 us with a vector per thread and shuffles between
+// the halves (75% of the issue slots busy), 52 us with two vectors per thread
+// at 80 registers, 43 us at 64 (6.2 TB/s); 48 registers spill and take 62 us.
+// The fused store of 16384 tokens of 32 + 8 + 8 rows (370 MB): 117, 86, 71 us.
 #pragma once
 
 #include <cstdint>
@@ -42,7 +44,7 @@ namespace mfp8 {
 namespace rope {
 
 constexpr int kThreads = 128;
-constexpr int kItems = 3;       // vector pairs per thread and pass, loads issued first
+constexpr int kBlocksPerSm = 8;  // 64 registers a thread: loads of 1024 threads in flight hide HBM's latency
 
 // Rows of a token, in order: nq rotated rows written to Y, nk rotated rows
 // quantized into the K pages, nv rows quantized into the V pages.  rot = 0
@@ -111,9 +113,10 @@ __device__ __forceinline__ void rotate_word(uint32_t& x, float c, float s) {
     x = *reinterpret_cast<const uint32_t*>(&y);
 }
 
-// UPR lanes per row, a power of two >= D / 16, two vectors each.
-template <int UPR, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads)
+// UPR lanes per row, a power of two >= D / 16, two vectors each; ITEMS rows
+// per thread and pass, their loads issued first.
+template <int UPR, bool INTERLEAVED, int ITEMS>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 rope_store_kernel(const Params p) {
     grid_launch_dependents();
     grid_dependency_wait();  // X may be the previous kernel's output
@@ -135,10 +138,10 @@ rope_store_kernel(const Params p) {
     const bool live = token < p.T && u < (p.vpr >> 1);
     const uint4* x = p.X + int64_t(token) * p.ldx;
 
-    uint4 a[kItems], b[kItems];
+    uint4 a[ITEMS], b[ITEMS];
     auto load = [&](int base) {
 #pragma unroll
-        for (int k = 0; k < kItems; ++k) {
+        for (int k = 0; k < ITEMS; ++k) {
             const int h = base + k * hstep;
             a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
             if (live && h < heads) {
@@ -181,10 +184,10 @@ rope_store_kernel(const Params p) {
         }
     }
     // every thread of a warp makes the same number of passes (the shuffles want them all)
-    for (int base = h0; base - h0 < heads; base += kItems * hstep) {
+    for (int base = h0; base - h0 < heads; base += ITEMS * hstep) {
         if (base != h0) load(base);
 #pragma unroll
-        for (int k = 0; k < kItems; ++k) {
+        for (int k = 0; k < ITEMS; ++k) {
             const int h = base + k * hstep;
             if (h - h0 >= heads) break;  // no thread has a row here
             const bool mine = live && h < heads;
@@ -216,11 +219,16 @@ rope_store_kernel(const Params p) {
                     const int hk = key ? h - p.nq : h - p.nq - p.nk;
                     const int64_t r = ((page * (key ? p.nk : p.nv) + hk) << p.ps_shift) + place;
                     const float sc = scale_from_absmax_bits(amax);
-                    const float rc = __frcp_rn(sc);
                     if (u == 0) (key ? p.k_scale : p.v_scale)[r] = sc;
                     uint2* q = (key ? p.K : p.V) + r * p.vpr;
-                    q[v0] = quantize8(a[k], sc, rc);
-                    q[v1] = quantize8(b[k], sc, rc);
+                    if (sc >= kFmaMinScale) {
+                        const float rc = __frcp_rn(sc);
+                        q[v0] = quantize8_fast(a[k], sc, rc);
+                        q[v1] = quantize8_fast(b[k], sc, rc);
+                    } else {
+                        q[v0] = quantize8_div_call(a[k], sc);
+                        q[v1] = quantize8_div_call(b[k], sc);
+                    }
                 }
             }
         }
