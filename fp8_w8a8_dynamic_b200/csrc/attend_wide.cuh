@@ -230,6 +230,15 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
     const uint32_t warp = warp_id_sync();
     const int lane = int(lane_id());
 
+    // What needs no input comes before the wait for the previous kernel.
+    if (warp == 13) {
+        tmem_alloc(smem_u32(tmem_holder), 512);
+        tmem_relinquish();
+    }
+    if (warp == 12 && lane == 0) {
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -253,7 +262,13 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
     }
     const int nrows = k.n * p.G;
     const int r0 = pair * kWideRows;
-    if (r0 >= nrows) return;
+    auto leave = [&] {  // before any barrier or MMA was used
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == 13) tmem_dealloc(*tmem_holder, 512);
+    };
+    if (r0 >= nrows) return leave();
     const bool both = nrows - r0 > kTile;  // the sides hold different rows
     const int rlast = min(r0 + kWideRows, nrows) - 1;
     const int seen = max(visible(k, rlast / p.G), 0);
@@ -272,12 +287,31 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             for (int i = threadIdx.x; i < (rlast - r0 + 1) * (D / 8); i += kWideThreads)
                 reinterpret_cast<uint4*>(p.O)[row_of(r0 + i / (D / 8)) * (D / 8) + i % (D / 8)] =
                     make_uint4(0u, 0u, 0u, 0u);
-        return;
+        return leave();
     }
     const int k0 = int(first), k1 = min(k0 + chunk, seen);
     const int nt = (k1 - k0 + kTile - 1) / kTile;
     const int steps = both ? 2 * nt : nt;  // step j: side j % 2, tile j / 2 (both) or j
 
+    // Each softmax warp's 32 query rows, as they are, to where V's f16 tiles will go: coalesced (a thread's own
+    // loads of its row would touch 32 lines an instruction, a bulk copy per row takes 70 cycles each), pieces
+    // swizzled by row.  Rows past the last are zeros.
+    const int side_row0 = r0 + (both && warp >= 4 ? kTile : 0) + int(warp & 3u) * 32;
+    const uint32_t q_stage = sb + L::C_OFF + warp * (32 * 2 * D);
+    if (warp < 8) {
+        constexpr int PR = D / 8;  // pieces per row
+        const int r = side_row0 + lane, t = r < nrows ? r / p.G : 0, g = r < nrows ? r - t * p.G : 0;
+        const int64_t mine = int64_t(k.tok0 + t) * p.ldq + int64_t(h * p.G + g) * D;  // this lane's row
+        const int piece = lane % PR;
+#pragma unroll 4
+        for (int i = 0; i < PR; ++i) {
+            const int rr = i * (32 / PR) + lane / PR;
+            const int64_t at = __shfl_sync(0xffffffffu, mine, rr);
+            cp_async16(q_stage + rr * (2 * D) + ((piece ^ (rr & (PR - 1))) << 4), p.Q + at + piece * 8,
+                       side_row0 + rr < nrows ? 16u : 0u);
+        }
+        cp_async_commit();
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::NUM_BARS; ++i) {
             uint32_t n = 1;
@@ -290,12 +324,6 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         }
         *abort_flag = 0;
         fence_mbar_init();
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-    }
-    if (warp == 13) {
-        tmem_alloc(smem_u32(tmem_holder), 512);
-        tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
@@ -307,20 +335,18 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         regs_inc<kSoftmaxRegs>();
         const int side = int(warp >> 2);
         const int i = int(threadIdx.x & 127);
-        const int r = r0 + (both ? side * kTile : 0) + i;
+        const int r = side_row0 + lane;
         const bool live = r < nrows;
         const int t = live ? r / p.G : 0;
         // Q: two e4m3 terms
         float f;
         {
-            const uint4* q = reinterpret_cast<const uint4*>(p.Q + int64_t(k.tok0 + t) * p.ldq +
-                                                            int64_t(h * p.G + (live ? r % p.G : 0)) * D);
-            uint4 x8[D / 8];  // every load of the row in flight at once
+            cp_async_wait<0>();
+            __syncwarp();
+            const uint32_t src = q_stage + uint32_t(lane) * (2 * D);
             uint32_t acc = 0;
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) x8[c] = live ? __ldg(q + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) acc = absmax_bits_u4(x8[c], acc);
+#pragma unroll 4
+            for (int c = 0; c < D / 8; ++c) acc = absmax_bits_u4(lds128(src + ((c ^ (lane & (D / 8 - 1))) << 4)), acc);
             const uint32_t amax = max(acc & 0xffffu, acc >> 16);
             // 2^e puts the largest element in [224, 448]: its exponent at 8, or at 7 above 1.75 * 2^n
             int e = max(int(amax >> 7), 10) - 127 - 8;
@@ -329,9 +355,10 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             f = fmaxf(p.scale_log2 * pow2i(e), kFltMin);
             const uint32_t hi = sb + L::Q_OFF + side * 2 * L::QB + i * D, lo = hi + L::QB;
             const uint32_t x = D == 128 ? uint32_t(i & 7) : uint32_t((i >> 1) & 3);
-#pragma unroll
+#pragma unroll 2
             for (int c = 0; c < D / 16; ++c) {
-                const uint4 a = x8[2 * c], b = x8[2 * c + 1];
+                const uint4 a = lds128(src + (((2 * c) ^ (lane & (D / 8 - 1))) << 4));
+                const uint4 b = lds128(src + (((2 * c + 1) ^ (lane & (D / 8 - 1))) << 4));
                 const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
                 uint32_t ch[4] = {0u, 0u, 0u, 0u}, cl[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -518,7 +545,8 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         constexpr int RPI = 128 / CH;  // tokens per pass
         const int ch = tid % CH;
         int vexp[2] = {kMinVexp, kMinVexp};  // of each side when they take alternate tiles
-        for (int tile = 0; tile < nt; ++tile) {
+        const bool free = wait_asleep(bar(L::QFULL), 0, abort_flag);  // the f16 tiles' place holds Q until then
+        for (int tile = 0; tile < nt && free; ++tile) {
             const int vs = tile % L::VST, cs = tile % L::CST;
             const int valid = min(kTile, k1 - (k0 + tile * kTile));
             if (!wait_asleep(bar(L::VFULL + vs), (tile / L::VST) & 1, abort_flag)) break;
