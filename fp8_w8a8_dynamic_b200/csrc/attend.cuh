@@ -549,44 +549,54 @@ join_kernel(const Params p) {
     const int t = int(row / p.Hq);
     if (t < p.q_start[0] || t >= p.q_start[p.B]) return;
     const int slots = p.splits_p + p.splits_o;
-    constexpr int VPL = D / 32;  // values per lane
-    float mx = -INFINITY;
-    for (int s = lane; s < slots; s += 32) mx = fmaxf(mx, p.part_lse[int64_t(s) * rows + row]);
+    constexpr int VPL = D / 32;     // values per lane
+    constexpr int kAhead = 8;       // slots whose loads are in flight together
+    const float* part = p.part + row * D + lane * VPL;
+    const int64_t pitch = rows * D;
+    auto load = [&](int s, float (&v)[VPL]) {
+        if constexpr (VPL == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(part + s * pitch);
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        } else {
+            const float2 x = *reinterpret_cast<const float2*>(part + s * pitch);
+            v[0] = x.x, v[1] = x.y;
+        }
+    };
+    // The first slots' outputs are asked for together with the log-sum-exps;
+    // what a slot without weight holds is not used.
+    float v[kAhead][VPL];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) v[i][j] = 0.0f;
+        if (i < slots) load(i, v[i]);
+    }
+    float lse0 = lane < slots ? p.part_lse[int64_t(lane) * rows + row] : -INFINITY;
+    float mx = lse0;
+    for (int s = lane + 32; s < slots; s += 32) mx = fmaxf(mx, p.part_lse[int64_t(s) * rows + row]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
     const float mz = mx == -INFINITY ? 0.0f : mx;
     float y[VPL], sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) y[j] = 0.0f;
-    constexpr int kAhead = 8;  // slots whose loads are in flight together
     for (int s0 = 0; s0 < slots; s0 += 32) {
-        const int s = s0 + lane;
-        const float w = s < slots ? ex2(p.part_lse[int64_t(s) * rows + row] - mz) : 0.0f;
+        if (s0 > 0) lse0 = s0 + lane < slots ? p.part_lse[int64_t(s0 + lane) * rows + row] : -INFINITY;
+        const float w = ex2(lse0 - mz);
         const int n = min(32, slots - s0);
         for (int i0 = 0; i0 < n; i0 += kAhead) {
-            float wi[kAhead], v[kAhead][VPL];
+            float wi[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 wi[i] = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
                 if (i0 + i >= n) wi[i] = 0.0f;
-                const float* src = p.part + (int64_t(s0 + i0 + i) * rows + row) * D + lane * VPL;
-#pragma unroll
-                for (int j = 0; j < VPL; ++j) v[i][j] = 0.0f;
-                if (wi[i] > 0.0f) {  // a slot without weight may hold anything
-                    if constexpr (VPL == 4) {
-                        const float4 x = *reinterpret_cast<const float4*>(src);
-                        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-                    } else {
-                        const float2 x = *reinterpret_cast<const float2*>(src);
-                        v[i][0] = x.x, v[i][1] = x.y;
-                    }
-                }
+                if (s0 + i0 > 0 && wi[i] > 0.0f) load(s0 + i0 + i, v[i]);
             }
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 sum += wi[i];
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) y[j] = fmaf(wi[i], v[i][j], y[j]);
+                for (int j = 0; j < VPL; ++j) y[j] = wi[i] > 0.0f ? fmaf(wi[i], v[i][j], y[j]) : y[j];
             }
         }
     }

@@ -907,13 +907,29 @@ struct AttendPlan {
 };
 
 constexpr int kAttendSms = 148;
+constexpr int kRowBlocks = 4;  // blocks per SM that the row kernel's splits aim at: 64 sequences of up to 1024 own
+                               // tokens took 95 us in all with 4, 101 with 8, 104 with 16; 256 of up to 4096: 283, 284, 301
 constexpr int64_t kAttendMax = int64_t(1) << 20;
-constexpr int64_t kWideFrom = 17;  // query rows per KV head from which the tall kernel takes a part
+
+// Which kernel takes a part (the prefix, or the own tokens) of `rows` query
+// rows per KV head, `units` KV heads (times sequences) and `len` tokens.  One
+// 16-row tile is the row kernel's whatever its length (own tokens of 4
+// sequences, 8 heads: 16384 tokens 42 us, tall 56).  With more rows the tall
+// kernel reads the tokens once for all of them, but its start costs 10 us;
+// both sides of the border, row kernel and tall kernel: 2048 prefix tokens,
+// 64 rows 12 / 15 us, 128 rows 20 / 15; 8192, 16 rows 14 / 18, 32 rows 23 /
+// 19; 65536, 128 rows 235 / 56; own tokens of 4 sequences, 512, 64 rows 13 /
+// 15, 128 rows 21 / 16; 2048, 32 rows 21 / 20.
+constexpr int64_t kWideWork = 100000;  // 16-row tiles times tokens
+bool attend_wide(int path, int64_t rows, int64_t units, int64_t len) {
+    if (path != MFP8_ATTEND_AUTO) return path == MFP8_ATTEND_TALL;
+    return rows > attend::kRows && (rows + attend::kRows - 1) / attend::kRows * units * len >= kWideWork;
+}
 
 // Row kernel: slots for `units` (row tile, KV head) pairs over `len` tokens:
 // enough blocks for four per SM, none with less than the smallest chunk.
 int attend_splits(int64_t units, int64_t len) {
-    int64_t s = (kAttendSms * 4 + units - 1) / units;
+    int64_t s = (kAttendSms * kRowBlocks + units - 1) / units;
     const int64_t most = (len + attend::kMinChunk - 1) / attend::kMinChunk;
     if (s > most) s = most;
     return int(s < 1 ? 1 : s > 256 ? 256 : s);
@@ -945,12 +961,12 @@ bool attend_shape_ok(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t Hk
 }
 
 AttendPlan attend_plan(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_len,
-                       int64_t max_pages, int64_t page_size) {
+                       int64_t max_pages, int64_t page_size, int path) {
     AttendPlan a;
     const int64_t G = Hq / Hkv;
     if (prefix_len > 0) {
         const int64_t rows = T * G;
-        a.wide_p = rows >= kWideFrom;
+        a.wide_p = attend_wide(path, rows, Hkv, prefix_len);
         const int64_t tile = a.wide_p ? attend::kWideRows : attend::kRows;
         a.tiles_p = (rows + tile - 1) / tile;
         a.splits_p = a.wide_p ? attend_wide_splits(a.tiles_p * Hkv, rows, prefix_len, T * Hq * D)
@@ -958,7 +974,7 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t 
     }
     if (max_pages > 0 || prefix_len == 0) {
         const int64_t rows = (max_q < T ? max_q : T) * G;
-        a.wide_o = rows >= kWideFrom && max_pages > 0;
+        a.wide_o = max_pages > 0 && attend_wide(path, rows, Hkv * B, max_pages * page_size);
         const int64_t tile = a.wide_o ? attend::kWideRows : attend::kRows;
         a.tiles_o = (rows + tile - 1) / tile;
         a.splits_o = a.wide_o ? attend_wide_splits(a.tiles_o * Hkv * B, rows, max_pages * page_size, T * Hq * D)
@@ -1603,7 +1619,12 @@ mfp8_status mfp8_rope_kv_store(const void* QKV_bf16, int64_t ldqkv, int64_t T, i
 size_t mfp8_prefix_attention_workspace_bytes(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D,
                                              int64_t prefix_len, int64_t max_pages, int64_t page_size) {
     if (!attend_shape_ok(T, B, max_q, Hq, Hkv, D, prefix_len, max_pages, page_size) || T == 0 || B == 0) return 0;
-    return attend_plan(T, B, max_q, Hq, Hkv, D, prefix_len, max_pages, page_size).total;
+    size_t most = 0;
+    for (int path = MFP8_ATTEND_AUTO; path <= MFP8_ATTEND_TALL; ++path) {
+        const size_t n = attend_plan(T, B, max_q, Hq, Hkv, D, prefix_len, max_pages, page_size, path).total;
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 mfp8_status mfp8_prefix_attention(const void* Q_bf16, int64_t ldq, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
@@ -1611,8 +1632,9 @@ mfp8_status mfp8_prefix_attention(const void* Q_bf16, int64_t ldq, int64_t T, in
                                   const void* k_pages, const float* k_scale, const void* v_pages, const float* v_scale,
                                   int64_t n_pages, int64_t page_size, const int32_t* prefix_pages, int64_t prefix_len,
                                   const int32_t* page_table, int64_t ld_table, int64_t max_pages, float softmax_scale,
-                                  void* O_bf16, float* lse, void* workspace, size_t workspace_bytes_given,
+                                  void* O_bf16, float* lse, void* workspace, size_t workspace_bytes_given, int path,
                                   void* stream) {
+    if (path < MFP8_ATTEND_AUTO || path > MFP8_ATTEND_TALL) return MFP8_ERR_INVALID_ARG;
     if (T < 0 || B < 0 || Hq < 0 || Hkv < 0 || D < 0 || ldq < 0 || max_q < 0 || n_pages < 0 || prefix_len < 0 ||
         max_pages < 0 || ld_table < 0 || !std::isfinite(softmax_scale) || !(softmax_scale > 0.0f))
         return MFP8_ERR_INVALID_ARG;
@@ -1630,7 +1652,7 @@ mfp8_status mfp8_prefix_attention(const void* Q_bf16, int64_t ldq, int64_t T, in
         !aligned16(v_scale) || !aligned_to(q_start) || !aligned_to(kv_len) || !aligned_to(prefix_pages) ||
         !aligned_to(page_table) || !aligned_to(lse))
         return MFP8_ERR_MISALIGNED;
-    const AttendPlan plan = attend_plan(T, B, max_q, Hq, Hkv, D, prefix_len, max_pages, page_size);
+    const AttendPlan plan = attend_plan(T, B, max_q, Hq, Hkv, D, prefix_len, max_pages, page_size, path);
     const size_t rows = size_t(n_pages) * size_t(Hkv * page_size);
     // inputs, then what is written
     const void* const buf[12] = {Q_bf16, k_pages, k_scale, v_pages, v_scale, q_start, kv_len, page_table, prefix_pages,

@@ -34,6 +34,10 @@ FLAG_STATIC_WEIGHTS = 1
 ROPE_HALF = 0
 ROPE_INTERLEAVED = 1
 
+ATTEND_AUTO = 0
+ATTEND_ROWS = 1
+ATTEND_TALL = 2
+
 ROPE_SCALE_NONE = 0
 ROPE_SCALE_LINEAR = 1
 ROPE_SCALE_NTK = 2
@@ -83,7 +87,7 @@ def lib():
                                          i64, i64, P]),
             "mfp8_prefix_attention_workspace_bytes": (sz, [i64] * 9),
             "mfp8_prefix_attention": (i32, [P, i64, i64, i64, i64, i64, P, P, i64, i64, P, P, P, P, i64, i64, P, i64,
-                                            P, i64, i64, f32, P, P, P, sz, P]),
+                                            P, i64, i64, f32, P, P, P, sz, i32, P]),
             "mfp8_debug_kv8_code_check": (i32, [P, i64, ctypes.c_uint32, P]),
             "mfp8_e4m3_encode_f32": (i32, [P, i64, P, P]),
             "mfp8_debug_quantize_check": (i32, [P, P]),
@@ -206,11 +210,11 @@ def mfp8_prefix_attention_workspace_bytes(T, B, max_q, Hq, Hkv, D, prefix_len, m
 
 def mfp8_prefix_attention(Q_bf16, ldq, T, Hq, Hkv, D, q_start, kv_len, B, max_q, k_pages, k_scale, v_pages, v_scale,
                           n_pages, page_size, prefix_pages, prefix_len, page_table, ld_table, max_pages,
-                          softmax_scale, O_bf16, lse, workspace, workspace_bytes, stream=0):
+                          softmax_scale, O_bf16, lse, workspace, workspace_bytes, path=0, stream=0):
     return lib().mfp8_prefix_attention(Q_bf16, ldq, T, Hq, Hkv, D, q_start, kv_len, B, max_q, k_pages, k_scale,
                                        v_pages, v_scale, n_pages, page_size, prefix_pages, prefix_len, page_table,
                                        ld_table, max_pages, softmax_scale, O_bf16, lse, workspace, workspace_bytes,
-                                       stream)
+                                       path, stream)
 
 
 def mfp8_debug_kv8_code_check(out, n_scale_pairs, seed, stream=0):
@@ -621,7 +625,7 @@ def _attention_workspace(*sizes):
 
 
 def prefix_attention(q, q_start, kv_len, page_table, prefix_pages, prefix_len, k_pages, k_scale, v_pages, v_scale,
-                     max_q, scale=None, out=None, want_lse=False, workspace=None, stream=None):
+                     max_q, scale=None, out=None, want_lse=False, workspace=None, path=ATTEND_AUTO, stream=None):
     """Attention of a batch that shares a prefix, over the paged FP8 cache.
     q bf16 [T, Hq, D] (tokens may be strided); q_start int32 [B + 1]: sequence
     b has the query tokens q_start[b] .. q_start[b + 1] - 1, at most max_q;
@@ -673,7 +677,7 @@ def prefix_attention(q, q_start, kv_len, page_table, prefix_pages, prefix_len, k
         q.data_ptr(), ldq, T, Hq, Hkv, D, q_start.data_ptr(), kv_len.data_ptr(), B, max_q, k_pages.data_ptr(),
         k_scale.data_ptr(), v_pages.data_ptr(), v_scale.data_ptr(), n_pages, ps, _ptr(prefix_pages), prefix_len,
         page_table.data_ptr() if max_pages else None, ld, max_pages, scale if scale is not None else D ** -0.5,
-        out.data_ptr(), _ptr(lse), _ptr(workspace), nbytes, handle), "mfp8_prefix_attention")
+        out.data_ptr(), _ptr(lse), _ptr(workspace), nbytes, path, handle), "mfp8_prefix_attention")
     return (out, lse) if want_lse else out
 
 

@@ -401,8 +401,15 @@ MFP8_API mfp8_status mfp8_rope_kv_store(const void* QKV_bf16, int64_t ldqkv, int
 
 /* ------------------------------------- attention over a shared prefix -- */
 
+/* Kernel choice for mfp8_prefix_attention. */
+typedef enum {
+    MFP8_ATTEND_AUTO = 0, /* chosen for the prefix and for the own tokens from their sizes */
+    MFP8_ATTEND_ROWS = 1, /* 16 query rows per KV head at a time: bound by reading the cache */
+    MFP8_ATTEND_TALL = 2  /* up to 256 at a time on the tcgen05 tensor cores */
+} mfp8_attend_path;
+
 /* Workspace bytes that are enough for mfp8_prefix_attention at these sizes
- * (0 for invalid ones): the fp32 partial outputs of the chunks that the
+ * with any kernel choice (0 for invalid sizes): the fp32 partial outputs of the chunks that the
  * tokens are cut into. */
 MFP8_API size_t mfp8_prefix_attention_workspace_bytes(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv,
                                                       int64_t D, int64_t prefix_len, int64_t max_pages,
@@ -435,6 +442,7 @@ MFP8_API size_t mfp8_prefix_attention_workspace_bytes(int64_t T, int64_t B, int6
  *       overlap an input.
  *   workspace: mfp8_prefix_attention_workspace_bytes(...) bytes, any
  *       contents; calls that may run at the same time need separate ones.
+ *   path: an mfp8_attend_path; results agree within the roundings below.
  * Lengths, pages and starts are read on the device, so a captured graph may
  * be replayed with new ones.  Values out of range are cut to what is in range
  * (a bad page reads page 0), and recorded as MFP8_ERR_INDEX in the device
@@ -452,7 +460,7 @@ MFP8_API mfp8_status mfp8_prefix_attention(const void* Q_bf16, int64_t ldq, int6
                                            int64_t page_size, const int32_t* prefix_pages, int64_t prefix_len,
                                            const int32_t* page_table, int64_t ld_table, int64_t max_pages,
                                            float softmax_scale, void* O_bf16, float* lse, void* workspace,
-                                           size_t workspace_bytes, void* stream);
+                                           size_t workspace_bytes, int path, void* stream);
 
 /* Diagnostic: checks the quantizer's divide-free arithmetic against IEEE
  * divides.  The scale fl32(absmax / 448) of every absmax (0 and each positive

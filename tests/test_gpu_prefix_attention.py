@@ -47,13 +47,26 @@ CASES = {
 }
 
 
+PATHS = (mfp8.ATTEND_ROWS, mfp8.ATTEND_TALL)
+
+
+@pytest.mark.parametrize("path", PATHS)
 @pytest.mark.parametrize("name", CASES)
-def test_against_64_bits(name):
+def test_against_64_bits(name, path):
     b = Batch(*CASES[name], seed=len(name))
-    out, lse, scale = run(b)
+    out, lse, scale = run(b, path=path)
     b.check(out, lse, scale, name)
-    plain = mfp8.prefix_attention(*b.args())
+    plain = mfp8.prefix_attention(*b.args(), path=path)
     assert torch.equal(plain, out)  # the same bits again, without lse and with the default scale
+
+
+def test_the_choice_by_size():
+    """Sizes on both sides of the border, each part's kernel its own: a large
+    batch's prefix with few own tokens, long prompts, and a small batch."""
+    for n, own, P in (([1] * 150, [9] * 150, 1500), ([400, 1, 333], [700, 5, 333], 900), ([1] * 3, [30] * 3, 800)):
+        b = Batch(n, own, P, 16, 4, 128, 32, seed=P)
+        out, lse, scale = run(b)
+        b.check(out, lse, scale, str(P))
 
 
 def test_strided_queries_rows_outside_and_workspace_contents():
@@ -78,14 +91,16 @@ def test_wide_table_strided_rows_and_longer_max_q():
     b.check(out, lse, scale)
 
 
+@pytest.mark.parametrize("path", PATHS)
 @pytest.mark.parametrize("k_gain,scale", [(30.0, 0.3), (1e-3, 1.0), (1.0, 1e-6), (8.0, 2.0)])
-def test_peaked_and_flat_rows(k_gain, scale):
+def test_peaked_and_flat_rows(k_gain, scale, path):
     b = Batch([1, 1, 4], [100, 3, 80], 700, 8, 2, 128, 16, seed=5, k_gain=k_gain)
-    out, lse, _ = run(b, scale)
+    out, lse, _ = run(b, scale, path=path)
     b.check(out, lse, scale)
 
 
-def test_value_scales_far_apart_and_zero_rows():
+@pytest.mark.parametrize("path", PATHS)
+def test_value_scales_far_apart_and_zero_rows(path):
     b = Batch([1, 2], [60, 40], 400, 8, 2, 128, 16, seed=6, v_spread=4.0)
     for sl in b.slots:  # rows of zeros take FLT_MIN as their scale
         z = sl[::5].cuda()
@@ -94,36 +109,39 @@ def test_value_scales_far_apart_and_zero_rows():
         z = sl[1::7].cuda()
         b.k_pages[z // 16, :, z % 16] = 0
         b.k_scale[z // 16, :, z % 16] = 2.0 ** -126
-    out, lse, scale = run(b)
+    out, lse, scale = run(b, path=path)
     b.check(out, lse, scale)
 
 
-def test_all_values_zero_or_tiny():
+@pytest.mark.parametrize("path", PATHS)
+def test_all_values_zero_or_tiny(path):
     b = Batch([1, 1], [9, 30], 40, 4, 2, 64, 8, seed=7)
     for sl in b.slots:
         s = sl.cuda()
         b.v_scale[s // 8, :, s % 8] *= 2.0 ** -80
-    out, lse, scale = run(b)
+    out, lse, scale = run(b, path=path)
     b.check(out, lse, scale)
     b.v_pages.zero_()
-    out, lse, scale = run(b)
+    out, lse, scale = run(b, path=path)
     assert (out == 0).all()
 
 
-def test_query_magnitudes():
+@pytest.mark.parametrize("path", PATHS)
+def test_query_magnitudes(path):
     b = Batch([1, 1, 1, 1], [9, 30, 2, 44], 120, 4, 2, 128, 8, seed=8)
     b.q[0] *= 2.0 ** -100
     b.q[1] = 0
     b.q[2, :, 5] = 3.0e4  # one element far above the others
     b.q[3] *= 2.0 ** -20
-    out, lse, scale = run(b)
+    out, lse, scale = run(b, path=path)
     b.check(out, lse, scale)
 
 
-def test_offsets_past_32_bits():
+@pytest.mark.parametrize("path", PATHS)
+def test_offsets_past_32_bits(path):
     H, ps, D = 8, 256, 128
     b = Batch([1, 1], [300, 30], 700, 16, H, D, ps, seed=9, wide_pool=2 ** 32 // (H * ps * D) + 9)
-    out, lse, scale = run(b)
+    out, lse, scale = run(b, path=path)
     b.check(out, lse, scale)
 
 
@@ -137,7 +155,8 @@ def test_other_stream():
     assert torch.equal(got, want) and torch.equal(lse, lse2)
 
 
-def test_graph_replayed_with_new_lengths_and_a_shared_workspace():
+@pytest.mark.parametrize("path", PATHS)
+def test_graph_replayed_with_new_lengths_and_a_shared_workspace(path):
     """Two captured graphs share a workspace and are replayed in turn; a replay
     follows lengths and pages that changed since the capture."""
     b = Batch([1] * 4, [40, 64, 1, 17], 300, 8, 2, 128, 16, seed=11, max_pages=8)
@@ -146,10 +165,10 @@ def test_graph_replayed_with_new_lengths_and_a_shared_workspace():
     ws = torch.empty((max(size),), dtype=torch.uint8, device="cuda")
     got = []
     for x in (b, c):
-        run(x, workspace=ws)
+        run(x, workspace=ws, path=path)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            out, lse, scale = run(x, workspace=ws)
+            out, lse, scale = run(x, workspace=ws, path=path)
         got.append((graph, out, lse))
     for _ in range(2):
         for graph, _, _ in got:
@@ -164,7 +183,11 @@ def test_graph_replayed_with_new_lengths_and_a_shared_workspace():
     b.check(got[0][1], got[0][2], scale)
 
 
-def test_lengths_and_pages_out_of_range_are_cut_and_reported():
+@pytest.mark.parametrize("path", PATHS)
+def test_lengths_and_pages_out_of_range_are_cut_and_reported(path):
+    def run(x):
+        return mfp8.prefix_attention(*x.args(), want_lse=True, path=path) + (x.D ** -0.5,)
+
     b = Batch([1, 1], [20, 20], 64, 4, 2, 64, 16, seed=13)
     want, lse, scale = run(b)
     table = b.page_table.clone()

@@ -148,11 +148,11 @@ def test_rope_kv_store_refused():
 
 BASE = dict(Q=F, ldq=1024, T=4, Hq=8, Hkv=2, D=128, qs=2 * F, kl=3 * F, B=4, mq=1, kp=16 * F, ks=32 * F, vp=48 * F,
             vs=64 * F, n=8, ps=16, pp=4 * F, P=40, pt=5 * F, ldt=2, mp=2, scale=0.1, O=6 * F, lse=None, ws=80 * F,
-            wsb=1 << 30)
+            wsb=1 << 30, path=0, stream=None)
 
 
 def attend(**kw):
-    return mfp8.mfp8_prefix_attention(*{**BASE, **kw}.values())
+    return mfp8.lib().mfp8_prefix_attention(*{**BASE, **kw}.values())
 
 
 def test_prefix_attention_refused():
@@ -160,7 +160,7 @@ def test_prefix_attention_refused():
     assert [attend(**k) for k in (dict(T=-1), dict(B=-1), dict(Q=None), dict(O=None), dict(qs=None), dict(kl=None),
                                   dict(pp=None), dict(pt=None), dict(kp=None), dict(vs=None), dict(n=0), dict(P=-1),
                                   dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan),
-                                  dict(scale=math.inf))] == [ARG] * 16
+                                  dict(scale=math.inf), dict(path=-1), dict(path=3))] == [ARG] * 18
     assert [attend(**k) for k in (dict(D=96), dict(D=256, ldq=2048), dict(Hq=7, ldq=896), dict(Hkv=0), dict(mq=0),
                                   dict(ldq=1016), dict(ldq=1028), dict(ps=20), dict(ldt=1), dict(T=1 << 21),
                                   dict(B=1 << 21), dict(P=1 << 31), dict(mp=1 << 30, ldt=1 << 30))] == [SHAPE] * 13
