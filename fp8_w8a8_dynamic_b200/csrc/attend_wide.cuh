@@ -49,8 +49,8 @@ namespace attend {
 constexpr int kWideThreads = 512;
 constexpr int kTile = 128;      // tokens per tile, rows per side
 constexpr int kWideRows = 256;  // rows per CTA
-constexpr float kLag = 4.0f;
-constexpr int kNorm = 11;     // P holds p 2^kNorm, below 2^15 in f16
+constexpr float kLag = 8.0f;  // octaves; with 4, a third of the tiles of a long prefix rescaled O in some warp, 420 cycles each
+constexpr int kNorm = 7;      // P holds p 2^kNorm, below 2^15 in f16
 constexpr int kVNorm = 7;     // V holds dec(V) sv / M 2^kVNorm, below 448 * 2^7
 constexpr int kMinVexp = 27;  // M >= 2^-100
 // Registers: 512 threads are launched with 128 each; the softmax warps, which
@@ -653,15 +653,17 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         constexpr uint32_t idesc_o = idesc_pv(D);
         bool any = false;
         int done[2] = {0, 0};  // P tiles consumed by each side
+        // Descriptors of a step are made once and moved by constants (an address is the low 14 bits, 16 bytes each,
+        // and stays below 227 KB): made anew for every MMA they cost the lane more than the MMA's 64 cycles.
         auto pv = [&](int side, int tile) {
             if (!wait_asleep(bar(L::PFULL + side), done[side] & 1, abort_flag)) return false;
             if (!wait_asleep(bar(L::CFULL + tile % L::CST), (tile / L::CST) & 1, abort_flag)) return false;
             tc_fence_after();
-            const uint32_t v = sb + L::C_OFF + (tile % L::CST) * kTile * D * 2;
+            const uint64_t v = nmajor_desc(sb + L::C_OFF + (tile % L::CST) * kTile * D * 2);
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk)
                 mma_f16_tmem_a(tmem + 256u + uint32_t(side) * 128u, tmem + uint32_t(side) * 128u + kk * 8,
-                               nmajor_desc(v + kk * 2048), idesc_o, (done[side] | kk) != 0);
+                               v + uint64_t(kk * 2048 >> 4), idesc_o, (done[side] | kk) != 0);
             any = true;
             ++done[side];
             if (!both || side == 1) mma_commit(bar(L::CEMPTY + tile % L::CST));
@@ -676,12 +678,11 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             ok = wait_asleep(bar(L::KFULL + ks), (tile / L::KST) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t kb = sb + L::K_OFF + ks * kTile * D, qb = sb + L::Q_OFF + side * 2 * L::QB;
+            const uint64_t kd = kmajor_desc<D>(sb + L::K_OFF + ks * kTile * D), qd = kmajor_desc<D>(sb + L::Q_OFF + side * 2 * L::QB);
 #pragma unroll
             for (int kk = 0; kk < 2 * (D / 32); ++kk) {
                 const uint32_t term = kk >= D / 32 ? uint32_t(L::QB) : 0u, off = uint32_t(kk % (D / 32)) * 32u;
-                mma_f8(tmem + uint32_t(side) * 128u, kmajor_desc<D>(qb + term + off), kmajor_desc<D>(kb + off), idesc_s,
-                       kk != 0);
+                mma_f8(tmem + uint32_t(side) * 128u, qd + ((term + off) >> 4), kd + (off >> 4), idesc_s, kk != 0);
             }
             any = true;
             mma_commit(bar(L::SFULL + side));
