@@ -657,7 +657,10 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         // and stays below 227 KB): made anew for every MMA they cost the lane more than the MMA's 64 cycles.
         auto pv = [&](int side, int tile) {
             if (!wait_asleep(bar(L::PFULL + side), done[side] & 1, abort_flag)) return false;
-            if (!wait_asleep(bar(L::CFULL + tile % L::CST), (tile / L::CST) & 1, abort_flag)) return false;
+            // (a tile that both sides use was waited for with side 0; a wait costs the lane 150 cycles even when what it
+            // waits for is long there)
+            if ((!both || side == 0) && !wait_asleep(bar(L::CFULL + tile % L::CST), (tile / L::CST) & 1, abort_flag))
+                return false;
             tc_fence_after();
             const uint64_t v = nmajor_desc(sb + L::C_OFF + (tile % L::CST) * kTile * D * 2);
 #pragma unroll
@@ -675,7 +678,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             if (j >= 2) ok = pv(side, both ? tile - 1 : tile - 2);
             if (!ok) break;
             const int ks = tile % L::KST;
-            ok = wait_asleep(bar(L::KFULL + ks), (tile / L::KST) & 1, abort_flag);
+            if (!both || side == 0) ok = wait_asleep(bar(L::KFULL + ks), (tile / L::KST) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
             const uint64_t kd = kmajor_desc<D>(sb + L::K_OFF + ks * kTile * D), qd = kmajor_desc<D>(sb + L::Q_OFF + side * 2 * L::QB);
