@@ -856,6 +856,15 @@ mfp8_status check_rope_args(const int32_t* pos, int n_axes, const uint8_t* axis,
     return MFP8_OK;
 }
 
+// Whether [out, out + n) overlaps the positions or tables of a rotation.
+bool over_rope_inputs(const void* out, size_t n, const int32_t* pos, int n_axes, int64_t T, const uint8_t* axis,
+                      const float* inv_freq, int64_t rot) {
+    if (rot == 0) return false;
+    return ranges_overlap(out, n, pos, size_t(n_axes) * size_t(T) * 4) ||
+           ranges_overlap(out, n, inv_freq, size_t(rot / 2) * 4) ||
+           (n_axes > 1 && ranges_overlap(out, n, axis, size_t(rot / 2)));
+}
+
 mfp8_status launch_rope(rope::Params p, int layout, cudaStream_t stream) {
     const int heads = p.nq + p.nk + p.nv;
     const int units = p.vpr / 2;
@@ -1475,6 +1484,8 @@ mfp8_status mfp8_rope(const void* X_bf16, int64_t ldx, int64_t T, int64_t H, int
     const bool in_place = X_bf16 == Y_bf16 && ldx == ldy;
     if (!in_place && ranges_overlap(X_bf16, strided_bytes(T, ldx, H * D, 2), Y_bf16, strided_bytes(T, ldy, H * D, 2)))
         return MFP8_ERR_INVALID_ARG;
+    if (over_rope_inputs(Y_bf16, strided_bytes(T, ldy, H * D, 2), pos, n_axes, T, axis, inv_freq, rot))
+        return MFP8_ERR_INVALID_ARG;
     int dev;
     DeviceInfo info;
     if ((st = current_device(&dev, &info)) != MFP8_OK) return st;
@@ -1588,6 +1599,8 @@ mfp8_status mfp8_rope_kv_store(const void* QKV_bf16, int64_t ldqkv, int64_t T, i
     for (int i = 0; i < 7; ++i)
         for (int j = i + 1 > 2 ? i + 1 : 2; j < 7; ++j)
             if (ranges_overlap(buf[i], len[i], buf[j], len[j])) return MFP8_ERR_INVALID_ARG;
+    for (int j = 2; j < 7; ++j)
+        if (over_rope_inputs(buf[j], len[j], pos, n_axes, T, axis, inv_freq, rot)) return MFP8_ERR_INVALID_ARG;
     int dev;
     DeviceInfo info;
     if ((st = current_device(&dev, &info)) != MFP8_OK) return st;
@@ -1636,7 +1649,7 @@ mfp8_status mfp8_prefix_attention(const void* Q_bf16, int64_t ldq, int64_t T, in
                                   void* stream) {
     if (path < MFP8_ATTEND_AUTO || path > MFP8_ATTEND_TALL) return MFP8_ERR_INVALID_ARG;
     if (T < 0 || B < 0 || Hq < 0 || Hkv < 0 || D < 0 || ldq < 0 || max_q < 0 || n_pages < 0 || prefix_len < 0 ||
-        max_pages < 0 || ld_table < 0 || !std::isfinite(softmax_scale) || !(softmax_scale > 0.0f))
+        max_pages < 0 || ld_table < 0 || !std::isfinite(softmax_scale * 1.4426950408889634f) || !(softmax_scale > 0.0f))
         return MFP8_ERR_INVALID_ARG;
     if (!attend_shape_ok(T, B, max_q, Hq, Hkv, D, prefix_len, max_pages, page_size) ||
         !page_shape_ok(n_pages, Hkv, page_size, D) || ldq < Hq * D || ldq % 8 != 0 || ldq > kMaxDim ||
@@ -1798,6 +1811,6 @@ const char* mfp8_status_string(mfp8_status status) {
     return "unknown status";
 }
 
-int mfp8_version(void) { return 100; }
+int mfp8_version(void) { return 200; }
 
 }  // extern "C"

@@ -437,7 +437,7 @@ MFP8_API size_t mfp8_prefix_attention_workspace_bytes(int64_t T, int64_t B, int6
  *       when max_pages is 0.  kv_len[b] is at most max_pages * page_size.
  *       The work is cut by max_pages, so a table as narrow as the longest
  *       sequence is the fastest.
- *   softmax_scale finite and > 0.
+ *   softmax_scale finite and > 0 (up to 2e38).
  *   O_bf16 [T][Hq][D]; lse [T][Hq] fp32 or NULL (written).  Neither may
  *       overlap an input.
  *   workspace: mfp8_prefix_attention_workspace_bytes(...) bytes, any
@@ -447,9 +447,9 @@ MFP8_API size_t mfp8_prefix_attention_workspace_bytes(int64_t T, int64_t B, int6
  * be replayed with new ones.  Values out of range are cut to what is in range
  * (a bad page reads page 0), and recorded as MFP8_ERR_INDEX in the device
  * status.  Sums, softmax statistics and partial outputs are fp32; the
- * probabilities times the value scales are rounded to 11 bits (f16 relative
- * to the largest value scale read, so what a row sees should have value
- * scales within 2^24 of the largest), the outputs once to bf16.
+ * probabilities and the value scales are rounded to 11 bits (f16, the value
+ * scales relative to the largest one read, so those that matter to a row
+ * should lie within 2^20 of it), the outputs once to bf16.
  * D is 64 or 128; Hq a multiple of Hkv; B, max_q and T up to 2^20, prefix_len
  * and max_pages * page_size up to 2^30, n_pages * Hkv * page_size below 2^31
  * (a layer of more than 128 GB).  T == 0 or B == 0 is a no-op. */

@@ -97,6 +97,9 @@ def test_rope_refused():
     assert call(Y=F + 16) == ARG                # shifted over the input
     assert call(Y=F, ldy=2048) == ARG           # in place with other strides
     assert call(Y=F + 4 * 2048 - 16) == ARG     # its last row
+    assert call(Y=2 * F) == ARG and call(Y=3 * F) == ARG  # over the positions, the table
+    assert call(Y=5 * F, n=2, axis=5 * F + 64) == ARG
+    assert call(Y=2 * F, rot=0, T=0) == OK
 
 
 def test_page_store_and_read_refused():
@@ -143,7 +146,7 @@ def test_rope_kv_store_refused():
     assert [call(**k) for k in (dict(X=F + 4), dict(Q=5 * F + 8), dict(kp=16 * F + 1), dict(vs=64 * F + 4),
                                 dict(slot=4 * F + 4))] == [ALIGN] * 5
     assert [call(**k) for k in (dict(Q=F), dict(vp=16 * F), dict(vs=32 * F + 16), dict(kp=5 * F),
-                                dict(ks=4 * F))] == [ARG] * 5
+                                dict(ks=4 * F), dict(Q=2 * F), dict(vp=3 * F))] == [ARG] * 7
 
 
 BASE = dict(Q=F, ldq=1024, T=4, Hq=8, Hkv=2, D=128, qs=2 * F, kl=3 * F, B=4, mq=1, kp=16 * F, ks=32 * F, vp=48 * F,
