@@ -14,7 +14,7 @@
 // normalised output and log-sum-exp go to the workspace in fp32, and
 // join_kernel weighs them together.
 //
-// attend_rows_kernel: row tiles of 16 on mma.sync (f16 operands, fp32 sums).
+// attend_rows_kernel: row tiles of 8 or 16 on mma.sync (f16 operands, fp32 sums).
 // It serves the calls that are bound by reading the cache (a decode step's
 // own tokens: G rows per KV head), where a 128-row tcgen05 tile would be
 // almost empty.  e4m3 codes are exact in f16.  Q goes to f16 with a power of two per
@@ -26,19 +26,16 @@
 //
 // Each warp streams its own share of the chunk, 32 tokens at a time, through
 // a ring of three cp.async stages of its own, so warps never wait for one
-// another until they merge at the end.  The dot products' summation order is
-// free, so each lane's operand fragments are whole 16-byte pieces of code
-// rows: the four lanes of a quad take 16 (of each 64) dimensions of a key
-// row, and the eight lanes of a column group take 16 dimensions each of four
-// value rows, whose bytes are paired by token with byte permutes.
+// another until they merge at the end.  Tokens (for z) and dimensions (for
+// the output) are the 16 rows of a matrix instruction, query rows its 8
+// columns, so a decode step's few rows (G <= 8) waste none of them: half the
+// products, exponentials and accumulators that 16 rows need.  The dot
+// products' summation order is free, so each lane's operand fragments are
+// whole 16-byte pieces of code rows: the four lanes of a quad take 16 (of each
+// 64) dimensions of a key row, and the eight lanes of a column group take 16
+// dimensions each of four value rows, whose bytes are paired by token with
+// byte permutes.  The probabilities change sides by 8 x 8 transposes.
 //
-// Own tokens of 256 sequences of 128 to 4096 (8 KV heads of 128, 1.1 GB): 215
-// us, 5.1 TB/s, 0.78 of the copy rate; two blocks of four warps per SM at 212
-// registers.  Three blocks with two stages: 300 us in all instead of 283 for
-// that batch, 92 instead of 95 for 64 sequences of up to 1024; blocks of two
-// warps 296 and 92, of one warp 290 to 345 and 90, and 10 to 11 us instead of
-// 9 for four sequences: what a block does besides its tokens (lengths, pages,
-// queries and the merge in turn, about 5 us) counts for more there.
 #pragma once
 
 #include <cstdint>
@@ -56,7 +53,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;    // query rows per tile
 constexpr int kIter = 32;    // tokens per warp and iteration
 constexpr int kStages = 3;
-constexpr int kMinChunk = kWarps * kIter * 2;  // tokens: below two iterations per warp a split costs more than it saves
+constexpr int kRowsBlocks = 2;  // per SM
+constexpr int kMinChunk = 256;  // tokens: below two iterations per warp a split costs more than it saves
 constexpr int64_t kMaxTokens = int64_t(1) << 30;  // of one sequence
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -86,6 +84,7 @@ struct Params {
     int tiles_p, tiles_o;    // row tiles
     int max_q;
     bool direct;  // one slot in all: write O and lse
+    bool beside;  // attend_rows_kernel behind attend_wide_kernel of the same call, whose last block only waits
 };
 
 // What a block of query rows attends to.
@@ -192,17 +191,24 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     return v;
 }
 
+// An 8 x 8 matrix of 16-bit values, two of a row per lane, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(v));
+    return y;
+}
+
 // The exponent that scales row values into [2^7, 2^8) from the largest
 // magnitude's bf16 bits (tiny rows are taken as 2^-119).
 __device__ __forceinline__ int row_exponent(uint32_t amax_bits) { return max(int(amax_bits >> 7), 8) - 127 - 7; }
 
-template <int D>
+template <int D, int ROWS>
 struct RowsLayout {
     static constexpr int CHUNKS = D / 16;                 // 16-byte pieces of a code row
     static constexpr int STAGE = 2 * kIter * D + 2 * kIter * 4;  // K, V, k_scale, v_scale
     static constexpr int RING = kStages * STAGE;
     static constexpr int OPITCH = D + 4;
-    static constexpr int MERGE = kWarps * kRows * OPITCH * 4 + kWarps * kRows * 4;
+    static constexpr int MERGE = kWarps * ROWS * OPITCH * 4 + kWarps * ROWS * 4;
     static constexpr int SMEM = kWarps * RING > MERGE ? kWarps * RING : MERGE;
 };
 
@@ -214,13 +220,21 @@ __device__ __forceinline__ uint32_t swz(uint32_t r) {
     return ((r & 6u) ^ ((r & 1u) << 2)) & uint32_t(D / 16 - 1);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kThreads, kRowsBlocks)
 attend_rows_kernel(const Params p) {
-    using L = RowsLayout<D>;
+    using L = RowsLayout<D, ROWS>;
+    constexpr int NB = ROWS / 8;
     extern __shared__ __align__(128) uint8_t smem[];
     grid_launch_dependents();
-    grid_dependency_wait();
+    // Beside the tall kernel there is nothing to wait for: its blocks let this
+    // grid start once they have waited themselves, so all that came before is
+    // there, and the two write different slots.  One block more than there is
+    // work waits for the tall kernel, so that this grid ends after it and
+    // join_kernel, which waits for this grid, sees both.
+    const bool waits = p.beside && blockIdx.x == gridDim.x - 1;
+    if (!p.beside || waits) grid_dependency_wait();
+    if (waits) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
 
@@ -245,9 +259,9 @@ attend_rows_kernel(const Params p) {
         k = own_task(p, int(u / p.tiles_o));
     }
     const int nrows = k.n * p.G;
-    const int r0 = tile * kRows;
+    const int r0 = tile * ROWS;
     if (r0 >= nrows) return;
-    const int rlast = min(r0 + kRows, nrows) - 1;
+    const int rlast = min(r0 + ROWS, nrows) - 1;
     const int seen = max(visible(k, rlast / p.G), 0);  // of the tile's last row, which sees most
     // Chunks of whole iterations of all warps; every chunk but the last is full.
     int chunk = (k.len + k.splits - 1) / k.splits;
@@ -255,7 +269,7 @@ attend_rows_kernel(const Params p) {
     const int64_t first = int64_t(split) * chunk;
     const int slot = k.slot0 + split;
     if (first >= seen) {  // nothing here
-        for (int i = threadIdx.x; i < kRows; i += kThreads) {
+        for (int i = threadIdx.x; i < ROWS; i += kThreads) {
             const int r = r0 + i;
             if (r < nrows) {
                 const int64_t row = int64_t(k.tok0 + r / p.G) * p.Hq + h * p.G + r % p.G;
@@ -264,7 +278,7 @@ attend_rows_kernel(const Params p) {
             }
         }
         if (p.direct)
-            for (int i = threadIdx.x; i < kRows * (D / 8); i += kThreads) {
+            for (int i = threadIdx.x; i < ROWS * (D / 8); i += kThreads) {
                 const int r = r0 + i / (D / 8);
                 if (r < nrows) {
                     const int64_t row = int64_t(k.tok0 + r / p.G) * p.Hq + h * p.G + r % p.G;
@@ -294,11 +308,13 @@ attend_rows_kernel(const Params p) {
             cp_async16(dst, p.K + at, n);
             cp_async16(dst + kIter * D, p.V + at, n);
         }
-        const int pg = __shfl_sync(0xffffffffu, page, lane >> 3);
+        const int pg = __shfl_sync(0xffffffffu, page, (lane % kIter) >> 3);
         const int64_t at = ((int64_t(pg) * p.Hkv + h) << p.ps_shift) + ((base + lane) & psm);
         const uint32_t n = base + lane < k1 ? 4u : 0u;
-        cp_async4(st + 2 * kIter * D + lane * 4, p.k_scale + at, n);
-        cp_async4(st + 2 * kIter * D + kIter * 4 + lane * 4, p.v_scale + at, n);
+        if (lane < kIter) {
+            cp_async4(st + 2 * kIter * D + lane * 4, p.k_scale + at, n);
+            cp_async4(st + 2 * kIter * D + kIter * 4 + lane * 4, p.v_scale + at, n);
+        }
     };
     auto page_at = [&](int it) { return it < iters ? page_of(p, k, k0 + it * kIter + 8 * c, k1 - 1) : 0; };
 
@@ -316,12 +332,12 @@ attend_rows_kernel(const Params p) {
     // ---- Q fragments: word w of a lane's codes is dimensions
     // (w / 4) * 64 + c * 16 + (w % 4) * 4 .. + 3 of the row
     constexpr int W = D / 16;
-    uint32_t qf[W][4];
-    float f[2];
-    int lim[2];
+    uint32_t qf[NB][W][2];
+    float f[NB][2];   // of columns 2c, 2c + 1 of z
+    int lim[NB][2];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int r = r0 + g + 8 * half;
+    for (int nb = 0; nb < NB; ++nb) {
+        const int r = r0 + g + 8 * nb;
         const bool live = r < nrows;
         const int t = live ? r / p.G : 0;
         const uint4* q = reinterpret_cast<const uint4*>(p.Q + int64_t(k.tok0 + t) * p.ldq +
@@ -343,111 +359,144 @@ attend_rows_kernel(const Params p) {
         const float m = pow2i(-e);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            qf[i][half] = pack_f16x2(bf16_lo(w[i][0]) * m, bf16_hi(w[i][0]) * m);
-            qf[i][2 + half] = pack_f16x2(bf16_lo(w[i][1]) * m, bf16_hi(w[i][1]) * m);
+            qf[nb][i][0] = pack_f16x2(bf16_lo(w[i][0]) * m, bf16_hi(w[i][0]) * m);
+            qf[nb][i][1] = pack_f16x2(bf16_lo(w[i][1]) * m, bf16_hi(w[i][1]) * m);
         }
-        f[half] = p.scale_log2 * pow2i(e);
-        lim[half] = live ? min(visible(k, t), k1) : 0;
+        const float fr = p.scale_log2 * pow2i(e);
+        const int lr = live ? min(visible(k, t), k1) : 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            f[nb][j] = __shfl_sync(0xffffffffu, fr, (2 * c + j) * 4);
+            lim[nb][j] = __shfl_sync(0xffffffffu, lr, (2 * c + j) * 4);
+        }
     }
     const int all_see = k.prefix ? k1 : min(visible(k, r0 / p.G), k1);  // tokens below are seen by every row
 
     // ---- the pass over the tokens
-    constexpr int NT = D / 8;  // column tiles of the output
-    float o[NT][4];
+    constexpr int MT = kIter / 16;  // 16-token tiles of an iteration
+    constexpr int NT = D / 8;       // dimensions of a lane group: g * NT ..
+    float o[NB][NT / 2][4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < NT / 2; ++i) o[nb][i][0] = o[nb][i][1] = o[nb][i][2] = o[nb][i][3] = 0.0f;
+    float m[NB][2], l[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.0f;
     int vexp = 27;  // biased exponent just above the largest value scale seen, at least 2^-100
 
     for (int it = warp; it < iters; it += kWarps) {
         cp_async_wait<kStages - 2>();
         __syncwarp();
         const uint32_t st = ring + uint32_t((it / kWarps) % kStages) * L::STAGE;
+        const uint32_t scales = st + 2 * kIter * D;
         const int base = k0 + it * kIter;
-        // z for 4 tiles of 8 tokens
-        float z[4][4];
+        // z: rows are tokens, columns query rows
+        float z[MT][NB][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            z[j][0] = z[j][1] = z[j][2] = z[j][3] = 0.0f;
-            const int r = j * 8 + g;
+        for (int t = 0; t < MT; ++t) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) z[t][nb][0] = z[t][nb][1] = z[t][nb][2] = z[t][nb][3] = 0.0f;
+            const int ra = t * 16 + g, rb = ra + 8;
 #pragma unroll
             for (int i = 0; i < W / 4; ++i) {
-                const uint4 code = lds128(st + r * D + (((c + 4 * i) ^ swz<D>(r)) << 4));
-                const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+                const uint4 ca = lds128(st + ra * D + (((c + 4 * i) ^ swz<D>(ra)) << 4));
+                const uint4 cb = lds128(st + rb * D + (((c + 4 * i) ^ swz<D>(rb)) << 4));
+                const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    mma_f16(z[j], qf[4 * i + e], f16x2_of_codes(uint16_t(w[e] & 0xffffu)),
-                            f16x2_of_codes(uint16_t(w[e] >> 16)));
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t a[4] = {
+                        f16x2_of_codes(uint16_t(wa[e] & 0xffffu)), f16x2_of_codes(uint16_t(wb[e] & 0xffffu)),
+                        f16x2_of_codes(uint16_t(wa[e] >> 16)), f16x2_of_codes(uint16_t(wb[e] >> 16))};
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) mma_f16(z[t][nb], a, qf[nb][4 * i + e][0], qf[nb][4 * i + e][1]);
+                }
             }
         }
-        float2 sv[4];
-        float mx[2] = {-INFINITY, -INFINITY};
+        float sv[MT][2];
+        float mx[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) mx[nb][0] = mx[nb][1] = -INFINITY;
         const bool masked = base + kIter > all_see;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t at = st + 2 * kIter * D + (j * 8 + 2 * c) * 4;
-            const uint2 a = lds64(at), b = lds64(at + kIter * 4);
-            sv[j] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
-            const float ka = __uint_as_float(a.x), kb = __uint_as_float(a.y);
-            z[j][0] *= ka * f[0];
-            z[j][1] *= kb * f[0];
-            z[j][2] *= ka * f[1];
-            z[j][3] *= kb * f[1];
-            if (masked) {
-                const int t = base + j * 8 + 2 * c;
-                if (t >= lim[0]) z[j][0] = -INFINITY;
-                if (t + 1 >= lim[0]) z[j][1] = -INFINITY;
-                if (t >= lim[1]) z[j][2] = -INFINITY;
-                if (t + 1 >= lim[1]) z[j][3] = -INFINITY;
+        for (int t = 0; t < MT; ++t) {
+            const uint32_t at = scales + (t * 16 + g) * 4;
+            const float ka = ld_shared_f32(at), kb = ld_shared_f32(at + 32);
+            sv[t][0] = ld_shared_f32(at + kIter * 4), sv[t][1] = ld_shared_f32(at + kIter * 4 + 32);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                float(&v)[4] = z[t][nb];
+                v[0] *= ka * f[nb][0];
+                v[1] *= ka * f[nb][1];
+                v[2] *= kb * f[nb][0];
+                v[3] *= kb * f[nb][1];
+                if (masked) {
+                    const int tok = base + t * 16 + g;
+                    if (tok >= lim[nb][0]) v[0] = -INFINITY;
+                    if (tok >= lim[nb][1]) v[1] = -INFINITY;
+                    if (tok + 8 >= lim[nb][0]) v[2] = -INFINITY;
+                    if (tok + 8 >= lim[nb][1]) v[3] = -INFINITY;
+                }
+                mx[nb][0] = fmaxf(mx[nb][0], fmaxf(v[0], v[2]));
+                mx[nb][1] = fmaxf(mx[nb][1], fmaxf(v[1], v[3]));
             }
-            mx[0] = fmaxf(mx[0], fmaxf(z[j][0], z[j][1]));
-            mx[1] = fmaxf(mx[1], fmaxf(z[j][2], z[j][3]));
         }
-        // largest value scale of the 32 tokens, as a power of two above it
-        const uint32_t svb = __reduce_max_sync(0xffffffffu, __float_as_uint(ld_shared_f32(st + 2 * kIter * D + kIter * 4 + lane * 4)));
+        // largest value scale of the iteration's tokens, as a power of two above it
+        const uint32_t svb = __reduce_max_sync(0xffffffffu, __float_as_uint(ld_shared_f32(scales + kIter * 4 + lane % kIter * 4)));
         const int ve = max(vexp, min(int(svb >> 23) + 1, 254));
         const float vadj = pow2i(max(vexp - ve, -126));
         const float vnorm = pow2i(14 - (ve - 127));
         vexp = ve;
-        float keep[2], mm[2];
+        float keep[NB][2], mm[NB][2];
+        bool moved = false;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 1));
-            mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 2));
-            const float mn = fmaxf(m[half], mx[half]);
-            mm[half] = mn == -INFINITY ? 0.0f : mn;  // nothing seen yet: every term is e^-inf = 0
-            keep[half] = ex2(m[half] - mm[half]);
-            m[half] = mn;
-            l[half] *= keep[half];
-            keep[half] *= vadj;
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float x = mx[nb][j];
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                const float mn = fmaxf(m[nb][j], x);
+                mm[nb][j] = mn == -INFINITY ? 0.0f : mn;  // nothing seen yet: every term is e^-inf = 0
+                keep[nb][j] = ex2(m[nb][j] - mm[nb][j]);
+                m[nb][j] = mn;
+                l[nb][j] *= keep[nb][j];
+                keep[nb][j] *= vadj;
+                moved = moved || keep[nb][j] != 1.0f;
+            }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < NT / 2; ++i) {
+                    o[nb][i][0] *= keep[nb][0];
+                    o[nb][i][1] *= keep[nb][1];
+                    o[nb][i][2] *= keep[nb][0];
+                    o[nb][i][3] *= keep[nb][1];
+                }
         }
-        if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
+        uint32_t pf[MT][NB][2];  // tokens by query rows, transposed into the layout of a second operand
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                o[i][0] *= keep[0];
-                o[i][1] *= keep[0];
-                o[i][2] *= keep[1];
-                o[i][3] *= keep[1];
+        for (int t = 0; t < MT; ++t) {
+            const float s0 = sv[t][0] * vnorm, s1 = sv[t][1] * vnorm;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const float a0 = ex2(z[t][nb][0] - mm[nb][0]), a1 = ex2(z[t][nb][1] - mm[nb][1]);
+                const float b0 = ex2(z[t][nb][2] - mm[nb][0]), b1 = ex2(z[t][nb][3] - mm[nb][1]);
+                l[nb][0] += a0 + b0;
+                l[nb][1] += a1 + b1;
+                pf[t][nb][0] = transpose8x8(pack_f16x2(a0 * s0, a1 * s0));
+                pf[t][nb][1] = transpose8x8(pack_f16x2(b0 * s1, b1 * s1));
             }
         }
-        uint32_t pf[2][4];
+        // output: rows g and g + 8 of tile i are dimensions g * NT + 2i and + 1, columns query rows
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float a0 = ex2(z[j][0] - mm[0]), a1 = ex2(z[j][1] - mm[0]);
-            const float b0 = ex2(z[j][2] - mm[1]), b1 = ex2(z[j][3] - mm[1]);
-            l[0] += a0 + a1;
-            l[1] += b0 + b1;
-            const float s0 = sv[j].x * vnorm, s1 = sv[j].y * vnorm;
-            pf[j >> 1][(j & 1) * 2] = pack_f16x2(a0 * s0, a1 * s1);
-            pf[j >> 1][(j & 1) * 2 + 1] = pack_f16x2(b0 * s0, b1 * s1);
-        }
-        // output: column tile i of lane group g is dimension g * NT + i
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            uint32_t a[4][NT / 4];  // value rows 2c, 2c + 1 of token tiles 2s and 2s + 1
+        for (int t = 0; t < MT; ++t) {
+            uint32_t a[4][NT / 4];  // value rows 2c, 2c + 1, 2c + 8, 2c + 9 of the token tile
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int r = (2 * s + (q >> 1)) * 8 + 2 * c + (q & 1);
+                const int r = (2 * t + (q >> 1)) * 8 + 2 * c + (q & 1);
                 const uint32_t row = st + kIter * D + r * D;
                 if constexpr (D == 128) {
                     const uint4 v = lds128(row + ((g ^ swz<D>(r)) << 4));
@@ -459,12 +508,15 @@ attend_rows_kernel(const Params p) {
             }
 #pragma unroll
             for (int q = 0; q < NT / 4; ++q) {
-                const uint32_t lo0 = __byte_perm(a[0][q], a[1][q], 0x5140), hi0 = __byte_perm(a[0][q], a[1][q], 0x7362);
-                const uint32_t lo1 = __byte_perm(a[2][q], a[3][q], 0x5140), hi1 = __byte_perm(a[2][q], a[3][q], 0x7362);
-                mma_f16(o[4 * q], pf[s], f16x2_of_codes(uint16_t(lo0 & 0xffffu)), f16x2_of_codes(uint16_t(lo1 & 0xffffu)));
-                mma_f16(o[4 * q + 1], pf[s], f16x2_of_codes(uint16_t(lo0 >> 16)), f16x2_of_codes(uint16_t(lo1 >> 16)));
-                mma_f16(o[4 * q + 2], pf[s], f16x2_of_codes(uint16_t(hi0 & 0xffffu)), f16x2_of_codes(uint16_t(hi1 & 0xffffu)));
-                mma_f16(o[4 * q + 3], pf[s], f16x2_of_codes(uint16_t(hi0 >> 16)), f16x2_of_codes(uint16_t(hi1 >> 16)));
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {  // dimensions 4q, 4q + 1, then 4q + 2, 4q + 3
+                    const uint32_t sel = half ? 0x7362u : 0x5140u;
+                    const uint32_t x = __byte_perm(a[0][q], a[1][q], sel), y = __byte_perm(a[2][q], a[3][q], sel);
+                    const uint32_t av[4] = {f16x2_of_codes(uint16_t(x & 0xffffu)), f16x2_of_codes(uint16_t(x >> 16)),
+                                            f16x2_of_codes(uint16_t(y & 0xffffu)), f16x2_of_codes(uint16_t(y >> 16))};
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) mma_f16(o[nb][2 * q + half], av, pf[t][nb][0], pf[t][nb][1]);
+                }
             }
         }
         __syncwarp();
@@ -479,32 +531,36 @@ attend_rows_kernel(const Params p) {
     cp_async_wait<0>();
     __syncthreads();  // every warp is done with its ring
     float* om = reinterpret_cast<float*>(smem);
-    float* lm = om + kWarps * kRows * L::OPITCH;
+    float* lm = om + kWarps * ROWS * L::OPITCH;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
-        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
-        const float inv = l[half] > 0.0f ? ldexpf(1.0f / l[half], vexp - 127 - 14) : 0.0f;
-        float* dst = om + (warp * kRows + g + 8 * half) * L::OPITCH + 2 * c * NT;
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            dst[i] = o[i][2 * half] * inv;
-            dst[NT + i] = o[i][2 * half + 1] * inv;
+        for (int j = 0; j < 2; ++j) {
+            float sum = l[nb][j];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+            const float inv = sum > 0.0f ? ldexpf(1.0f / sum, vexp - 127 - 14) : 0.0f;
+            const int i0 = warp * ROWS + nb * 8 + 2 * c + j;
+            float4* dst = reinterpret_cast<float4*>(om + i0 * L::OPITCH + g * NT);
+#pragma unroll
+            for (int i = 0; i < NT / 2; i += 2)
+                dst[i / 2] = make_float4(o[nb][i][j] * inv, o[nb][i][2 + j] * inv, o[nb][i + 1][j] * inv,
+                                         o[nb][i + 1][2 + j] * inv);
+            if (g == 0) lm[i0] = sum > 0.0f ? m[nb][j] + log2f(sum) : -INFINITY;
         }
-        if (c == 0) lm[warp * kRows + g + 8 * half] = l[half] > 0.0f ? m[half] + log2f(l[half]) : -INFINITY;
-    }
     __syncthreads();
-    constexpr int CPT = kRows * D / kThreads;  // values per thread, all of one row
+    constexpr int CPT = ROWS * D / kThreads;  // values per thread, all of one row
     const int i = threadIdx.x / (D / CPT), d0 = (threadIdx.x % (D / CPT)) * CPT;
     const int r = r0 + i;
     if (r >= nrows) return;
     float mx = lm[i];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, lm[w * kRows + i]);
+    for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, lm[w * ROWS + i]);
     const float mz = mx == -INFINITY ? 0.0f : mx;
     float wt[kWarps], sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += wt[w] = ex2(lm[w * kRows + i] - mz);
+    for (int w = 0; w < kWarps; ++w) sum += wt[w] = ex2(lm[w * ROWS + i] - mz);
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     const float out_lse = sum > 0.0f ? mx + log2f(sum) : -INFINITY;
     const int64_t row = int64_t(k.tok0 + r / p.G) * p.Hq + h * p.G + r % p.G;
@@ -515,22 +571,20 @@ attend_rows_kernel(const Params p) {
     for (int w = 0; w < kWarps; ++w)
 #pragma unroll
         for (int j = 0; j < CPT; j += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(om + (w * kRows + i) * L::OPITCH + d0 + j);
+            const float4 v = *reinterpret_cast<const float4*>(om + (w * ROWS + i) * L::OPITCH + d0 + j);
             y[j] = fmaf(wt[w], v.x, y[j]);
             y[j + 1] = fmaf(wt[w], v.y, y[j + 1]);
             y[j + 2] = fmaf(wt[w], v.z, y[j + 2]);
             y[j + 3] = fmaf(wt[w], v.w, y[j + 3]);
         }
     if (p.direct) {
-        uint32_t pk[CPT / 2];
+        uint2* dst = reinterpret_cast<uint2*>(p.O + row * D + d0);
 #pragma unroll
-        for (int j = 0; j < CPT; j += 2) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(y[j] * inv, y[j + 1] * inv);
-            pk[j / 2] = *reinterpret_cast<const uint32_t*>(&b);
+        for (int j = 0; j < CPT; j += 4) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(y[j] * inv, y[j + 1] * inv);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(y[j + 2] * inv, y[j + 3] * inv);
+            dst[j / 4] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
         }
-        uint4* dst = reinterpret_cast<uint4*>(p.O + row * D + d0);
-#pragma unroll
-        for (int j = 0; j < CPT / 8; ++j) dst[j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
         if (d0 == 0 && p.lse) p.lse[row] = out_lse * kLn2;
     } else {
         const int64_t at = int64_t(slot) * p.T * p.Hq + row;

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -912,6 +913,7 @@ struct AttendPlan {
     int splits_p = 0, splits_o = 0;
     int64_t tiles_p = 0, tiles_o = 0;
     bool direct = false;
+    bool few_rows = false;  // row kernel: no tile has more than 8 rows
     size_t lse_off = 0, total = 0;
 };
 
@@ -929,10 +931,10 @@ constexpr int64_t kAttendMax = int64_t(1) << 20;
 // 64 rows 12 / 15 us, 128 rows 20 / 15; 8192, 16 rows 14 / 18, 32 rows 23 /
 // 19; 65536, 128 rows 235 / 56; own tokens of 4 sequences, 512, 64 rows 13 /
 // 15, 128 rows 21 / 16; 2048, 32 rows 21 / 20.
-constexpr int64_t kWideWork = 100000;  // 16-row tiles times tokens
+constexpr double kWideWork = 100000;  // 16-row tiles times tokens
 bool attend_wide(int path, int64_t rows, int64_t units, int64_t len) {
     if (path != MFP8_ATTEND_AUTO) return path == MFP8_ATTEND_TALL;
-    return rows > attend::kRows && (rows + attend::kRows - 1) / attend::kRows * units * len >= kWideWork;
+    return rows > attend::kRows && double((rows + attend::kRows - 1) / attend::kRows * units) * double(len) >= kWideWork;
 }
 
 // Row kernel: slots for `units` (row tile, KV head) pairs over `len` tokens:
@@ -944,19 +946,25 @@ int attend_splits(int64_t units, int64_t len) {
     return int(s < 1 ? 1 : s > 256 ? 256 : s);
 }
 
-// Tall kernel, one CTA per SM: the number of slots whose whole waves of CTAs
-// take the fewest tile steps (1.2 us each), counting what a CTA does besides
-// (Q, the ends of the pipeline, its partial output: about 10 us) as eight,
-// and the writing and joining of one slot's outputs at 4 TB/s.
-int attend_wide_splits(int64_t units, int64_t rows, int64_t len, int64_t out_values) {
+// Tall kernel, one CTA per SM: the number of slots that ends first, counted
+// in tile steps (1.2 us each).  Its waves of CTAs take their steps and eight
+// more (Q, the ends of the pipeline, the partial output: about 10 us); the
+// row kernel's part of the call, `beside` bytes of cache, is read meanwhile
+// by the SMs that the tall kernel leaves (FREE), then by all (FULL); a slot's outputs are written
+// and joined at 4 TB/s.
+int attend_wide_splits(int64_t units, int64_t rows, int64_t len, int64_t out_values, double beside) {
+    constexpr double kStepUs = 1.2, kFree = 90e3, kFull = 5.1e6;  // bytes per us
     const int64_t tiles = (len + attend::kTile - 1) / attend::kTile;
     const int64_t per_tile = rows > attend::kTile ? 2 : 1;
-    const int64_t slot_cost = out_values * 8 / 4800;  // thousandths of a step: 8 bytes a value at 4 TB/s, of 1.2 us
-    int64_t best = 1, best_cost = INT64_MAX;
+    int64_t best = 1;
+    double best_us = 1e300;
     for (int64_t s = 1; s <= 64 && s <= tiles; ++s) {
         const int64_t waves = (units * s + kAttendSms - 1) / kAttendSms;
-        const int64_t cost = waves * ((tiles + s - 1) / s * per_tile + 8) * 1000 + s * slot_cost;
-        if (cost < best_cost) best = s, best_cost = cost;
+        const double tall = double(waves * ((tiles + s - 1) / s * per_tile + 8)) * kStepUs;
+        const int64_t idle = waves == 1 ? kAttendSms - units * s : 0;
+        const double rate = std::min(double(idle) * kFree, kFull);
+        const double us = tall + std::max(0.0, beside - tall * rate) / kFull + double(s * out_values) * 8 / 4e6;
+        if (us < best_us) best = s, best_us = us;
     }
     return int(best);
 }
@@ -972,23 +980,24 @@ bool attend_shape_ok(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t Hk
 AttendPlan attend_plan(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_len,
                        int64_t max_pages, int64_t page_size, int path) {
     AttendPlan a;
-    const int64_t G = Hq / Hkv;
-    if (prefix_len > 0) {
-        const int64_t rows = T * G;
-        a.wide_p = attend_wide(path, rows, Hkv, prefix_len);
-        const int64_t tile = a.wide_p ? attend::kWideRows : attend::kRows;
-        a.tiles_p = (rows + tile - 1) / tile;
-        a.splits_p = a.wide_p ? attend_wide_splits(a.tiles_p * Hkv, rows, prefix_len, T * Hq * D)
+    const int64_t G = Hq / Hkv, rows_p = T * G, rows_o = (max_q < T ? max_q : T) * G, len_o = max_pages * page_size;
+    const bool own = max_pages > 0 || prefix_len == 0;
+    a.wide_p = prefix_len > 0 && attend_wide(path, rows_p, Hkv, prefix_len);
+    a.wide_o = max_pages > 0 && attend_wide(path, rows_o, Hkv * B, len_o);
+    const int64_t tile_p = a.wide_p ? attend::kWideRows : attend::kRows;
+    const int64_t tile_o = a.wide_o ? attend::kWideRows : attend::kRows;
+    if (prefix_len > 0) a.tiles_p = (rows_p + tile_p - 1) / tile_p;
+    if (own) a.tiles_o = (rows_o + tile_o - 1) / tile_o;
+    // What the row kernel reads; own tokens are taken to fill half of the table.
+    const double bytes_p = a.wide_p ? 0.0 : double(a.tiles_p * Hkv) * double(prefix_len * 2 * (D + 4));
+    const double bytes_o = a.wide_o ? 0.0 : double(a.tiles_o * Hkv * B) * double(len_o * (D + 4));
+    if (prefix_len > 0)
+        a.splits_p = a.wide_p ? attend_wide_splits(a.tiles_p * Hkv, rows_p, prefix_len, T * Hq * D, bytes_o)
                               : attend_splits(a.tiles_p * Hkv, prefix_len);
-    }
-    if (max_pages > 0 || prefix_len == 0) {
-        const int64_t rows = (max_q < T ? max_q : T) * G;
-        a.wide_o = max_pages > 0 && attend_wide(path, rows, Hkv * B, max_pages * page_size);
-        const int64_t tile = a.wide_o ? attend::kWideRows : attend::kRows;
-        a.tiles_o = (rows + tile - 1) / tile;
-        a.splits_o = a.wide_o ? attend_wide_splits(a.tiles_o * Hkv * B, rows, max_pages * page_size, T * Hq * D)
-                              : attend_splits(a.tiles_o * Hkv * B, max_pages * page_size);
-    }
+    if (own)
+        a.splits_o = a.wide_o ? attend_wide_splits(a.tiles_o * Hkv * B, rows_o, len_o, T * Hq * D, bytes_p)
+                              : attend_splits(a.tiles_o * Hkv * B, len_o);
+    a.few_rows = (a.wide_p || prefix_len == 0 || rows_p <= 8) && (a.wide_o || rows_o <= 8);
     const int64_t slots = a.splits_p + a.splits_o;
     a.direct = slots == 1;
     if (!a.direct) {
@@ -1013,14 +1022,17 @@ mfp8_status make_map_pages(CUtensorMap* map, const void* base, int64_t rows, int
 
 template <int D>
 mfp8_status launch_attend(attend::Params p, const AttendPlan& plan, int dev, cudaStream_t stream) {
-    using L = attend::RowsLayout<D>;
+    using L8 = attend::RowsLayout<D, 8>;
+    using L16 = attend::RowsLayout<D, 16>;
     using WL = attend::WideLayout<D>;
     static bool ready[kMaxDevices] = {};
     {
         std::lock_guard<std::mutex> lock(g_mu);
         if (!ready[dev]) {
-            if (cudaFuncSetAttribute(attend::attend_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     L::SMEM) != cudaSuccess ||
+            if (cudaFuncSetAttribute(attend::attend_rows_kernel<D, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     L8::SMEM) != cudaSuccess ||
+                cudaFuncSetAttribute(attend::attend_rows_kernel<D, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     L16::SMEM) != cudaSuccess ||
                 cudaFuncSetAttribute(attend::attend_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      WL::SMEM_BYTES) != cudaSuccess) {
                 cudaGetLastError();
@@ -1047,7 +1059,10 @@ mfp8_status launch_attend(attend::Params p, const AttendPlan& plan, int dev, cud
     if (narrow > 0) {
         p.tiles_p = plan.wide_p ? 0 : int(plan.tiles_p);
         p.tiles_o = plan.wide_o ? 0 : int(plan.tiles_o);
-        st = launch_pdl(attend::attend_rows_kernel<D>, dim3(unsigned(narrow)), attend::kThreads, stream, L::SMEM, p);
+        p.beside = wide > 0;
+        const dim3 grid(unsigned(narrow + (wide > 0)));
+        st = plan.few_rows ? launch_pdl(attend::attend_rows_kernel<D, 8>, grid, attend::kThreads, stream, L8::SMEM, p)
+                           : launch_pdl(attend::attend_rows_kernel<D, 16>, grid, attend::kThreads, stream, L16::SMEM, p);
         if (st != MFP8_OK) return st;
     }
     if (p.direct) return MFP8_OK;
@@ -1682,7 +1697,7 @@ mfp8_status mfp8_prefix_attention(const void* Q_bf16, int64_t ldq, int64_t T, in
         for (int i = 0; i < j; ++i)
             if (len[i] && len[j] && ranges_overlap(buf[i], len[i], buf[j], len[j])) return MFP8_ERR_INVALID_ARG;
     const int64_t np = plan.tiles_p * plan.splits_p * Hkv, no = plan.tiles_o * plan.splits_o * Hkv * B;
-    if (np + no > INT32_MAX || int64_t(rows) > INT32_MAX) return MFP8_ERR_UNSUPPORTED_SHAPE;
+    if (np + no >= INT32_MAX || int64_t(rows) > INT32_MAX) return MFP8_ERR_UNSUPPORTED_SHAPE;
     int dev;
     DeviceInfo info;
     mfp8_status st = current_device(&dev, &info);
