@@ -183,6 +183,51 @@ def test_graph_replayed_with_new_lengths_and_a_shared_workspace(path):
     b.check(got[0][1], got[0][2], scale)
 
 
+@pytest.mark.parametrize("n,own,P,Hq", [
+    ([1] * 80, [9, 700] * 40, 6000, 8),  # tall prefix, own tokens in 8-row tiles beside it
+    ([1] * 80, [9, 700] * 40, 1500, 32),  # ... in 16-row tiles
+    ([400, 1, 200], [700, 5, 200], 24, 8),  # tall own tokens, the prefix beside them
+])
+def test_layers_in_a_row_with_both_kernels(n, own, P, Hq):
+    """Calls whose two kernels run beside each other, each reading the output
+    of the one before and all with one workspace: the bits of the same calls
+    with a synchronisation and fresh memory between them, eager and replayed."""
+    b = Batch(n, own, P, Hq, 2, 128, 64, seed=P)
+    size = mfp8.mfp8_prefix_attention_workspace_bytes(b.T, b.B, b.max_q, Hq, 2, 128, P, b.page_table.shape[1], 64)
+    ws = torch.zeros((size,), dtype=torch.uint8, device="cuda")
+    rest = b.args()[1:]
+    first = b.args()[0].contiguous()
+    bufs = [torch.zeros_like(first) for _ in range(6)]
+
+    def layers(x):
+        for y in bufs:
+            mfp8.prefix_attention(x, *rest, workspace=ws, out=y)
+            x = y
+
+    def separate(x):
+        ys = []
+        for _ in bufs:
+            x = mfp8.prefix_attention(x, *rest, out=torch.zeros_like(first))
+            torch.cuda.synchronize()
+            ys.append(x)
+        return ys
+
+    out, lse, scale = run(b)
+    b.check(out, lse, scale)
+    want = separate(first)
+    layers(first)
+    assert all(torch.equal(x, y) for x, y in zip(bufs, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layers(first)
+    for k in range(3):
+        first.mul_(-0.5)
+        want = separate(first)
+        ws.fill_(255)
+        graph.replay()
+        assert all(torch.equal(x, y) for x, y in zip(bufs, want)), k
+
+
 @pytest.mark.parametrize("path", PATHS)
 def test_lengths_and_pages_out_of_range_are_cut_and_reported(path):
     def run(x):
