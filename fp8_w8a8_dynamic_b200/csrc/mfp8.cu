@@ -906,32 +906,41 @@ mfp8_status launch_rope(rope::Params p, int layout, cudaStream_t stream) {
 // ------------------------------------- attention over a shared prefix --
 
 // How the work is cut: which kernel takes the prefix and the own tokens, the
-// slots of partial outputs per row of each, and their row tiles (of 16 rows,
-// or of 256 for the tall kernel).
+// slots of partial outputs per row of each, and their row tiles (of 8 or 16
+// rows, or of 256 for the tall kernel).
 struct AttendPlan {
     bool wide_p = false, wide_o = false;
     int splits_p = 0, splits_o = 0;
     int64_t tiles_p = 0, tiles_o = 0;
     bool direct = false;
-    bool few_rows = false;  // row kernel: no tile has more than 8 rows
+    int row_tile = 16;  // of the row kernel
     size_t lse_off = 0, total = 0;
 };
 
 constexpr int kAttendSms = 148;
-constexpr int kRowBlocks = 4;  // blocks per SM that the row kernel's splits aim at: 64 sequences of up to 1024 own
-                               // tokens took 95 us in all with 4, 101 with 8, 104 with 16; 256 of up to 4096: 283, 284, 301
+// Blocks per SM that the row kernel's splits aim at: 64 sequences of up to
+// 1024 own tokens took 78 us in all with 4 and with 6, 82 with 8; 256 of up
+// to 4096: 218, 219, 217.
+constexpr int kRowBlocks = 4;
 constexpr int64_t kAttendMax = int64_t(1) << 20;
 
 // Which kernel takes a part (the prefix, or the own tokens) of `rows` query
 // rows per KV head, `units` KV heads (times sequences) and `len` tokens.  One
 // 16-row tile is the row kernel's whatever its length (own tokens of 4
-// sequences, 8 heads: 16384 tokens 42 us, tall 56).  With more rows the tall
+// sequences, 8 heads: 16384 tokens 42 us, tall 57).  With more rows the tall
 // kernel reads the tokens once for all of them, but its start costs 10 us;
 // both sides of the border, row kernel and tall kernel: 2048 prefix tokens,
-// 64 rows 12 / 15 us, 128 rows 20 / 15; 8192, 16 rows 14 / 18, 32 rows 23 /
-// 19; 65536, 128 rows 235 / 56; own tokens of 4 sequences, 512, 64 rows 13 /
-// 15, 128 rows 21 / 16; 2048, 32 rows 21 / 20.
+// 64 rows 12 / 15 us, 128 rows 21 / 15; 8192, 16 rows 14 / 19, 32 rows 22 /
+// 19; 65536, 128 rows 223 / 57; own tokens of 4 sequences, 512, 64 rows 12 /
+// 15, 128 rows 21 / 16; 2048, 16 rows 12 / 19, 32 rows 21 / 20.
 constexpr double kWideWork = 100000;  // 16-row tiles times tokens
+// Row tiles of 8 where no part has more rows, or where the call is so short
+// that their start (2 us less than of 16 rows) counts for more than reading
+// the tokens twice; both sides, 16 and 8 rows per tile: 2048 prefix tokens, 32
+// rows 10.5 / 8.7 us, 64 rows 12.3 / 14.0; 8192, 16 rows 14.5 / 16.0; own
+// tokens of 4 sequences, 1024, 16 rows 11.4 / 9.1, 32 rows 12.6 / 14.7; 2048,
+// 16 rows 12.4 / 14.9.
+constexpr double kEightWork = 40000;  // 16-row tiles times tokens
 bool attend_wide(int path, int64_t rows, int64_t units, int64_t len) {
     if (path != MFP8_ATTEND_AUTO) return path == MFP8_ATTEND_TALL;
     return rows > attend::kRows && double((rows + attend::kRows - 1) / attend::kRows * units) * double(len) >= kWideWork;
@@ -946,14 +955,15 @@ int attend_splits(int64_t units, int64_t len) {
     return int(s < 1 ? 1 : s > 256 ? 256 : s);
 }
 
-// Tall kernel, one CTA per SM: the number of slots that ends first, counted
-// in tile steps (1.2 us each).  Its waves of CTAs take their steps and eight
-// more (Q, the ends of the pipeline, the partial output: about 10 us); the
-// row kernel's part of the call, `beside` bytes of cache, is read meanwhile
-// by the SMs that the tall kernel leaves (FREE), then by all (FULL); a slot's outputs are written
-// and joined at 4 TB/s.
+// Tall kernel, one CTA per SM: the number of slots that ends first.  A wave of
+// CTAs takes its tile steps and eight more (Q, the ends of the pipeline, the
+// partial output: about 10 us); the row kernel's part of the call, `beside`
+// bytes of cache, is read meanwhile by the SMs that the tall kernel leaves
+// free, then by all; a slot's outputs are written and joined at 4 TB/s.  64
+// sequences over 32768 shared tokens (8 units), slots and us: 12 86, 14 77, 16
+// 78, 18 79; 256 over 8192 (32 units), 1 218, 2 228, 3 232, 4 237.
 int attend_wide_splits(int64_t units, int64_t rows, int64_t len, int64_t out_values, double beside) {
-    constexpr double kStepUs = 1.2, kFree = 90e3, kFull = 5.1e6;  // bytes per us
+    constexpr double kStepUs = 1.2, kFree = 45e3, kFull = 5.4e6;  // bytes per us: one SM of a few, all
     const int64_t tiles = (len + attend::kTile - 1) / attend::kTile;
     const int64_t per_tile = rows > attend::kTile ? 2 : 1;
     int64_t best = 1;
@@ -984,8 +994,14 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t 
     const bool own = max_pages > 0 || prefix_len == 0;
     a.wide_p = prefix_len > 0 && attend_wide(path, rows_p, Hkv, prefix_len);
     a.wide_o = max_pages > 0 && attend_wide(path, rows_o, Hkv * B, len_o);
-    const int64_t tile_p = a.wide_p ? attend::kWideRows : attend::kRows;
-    const int64_t tile_o = a.wide_o ? attend::kWideRows : attend::kRows;
+    // The row kernel's work in 16-row tiles times tokens.
+    auto work = [](int64_t rows, int64_t units, int64_t len) { return double((rows + 15) / 16 * units) * double(len); };
+    const bool narrow_p = prefix_len > 0 && !a.wide_p, narrow_o = own && !a.wide_o;
+    if ((!narrow_p || rows_p <= 8) && (!narrow_o || rows_o <= 8)) a.row_tile = 8;
+    if ((narrow_p ? work(rows_p, Hkv, prefix_len) : 0.0) + (narrow_o ? work(rows_o, Hkv * B, len_o) : 0.0) <= kEightWork)
+        a.row_tile = 8;
+    const int64_t tile_p = a.wide_p ? attend::kWideRows : a.row_tile;
+    const int64_t tile_o = a.wide_o ? attend::kWideRows : a.row_tile;
     if (prefix_len > 0) a.tiles_p = (rows_p + tile_p - 1) / tile_p;
     if (own) a.tiles_o = (rows_o + tile_o - 1) / tile_o;
     // What the row kernel reads; own tokens are taken to fill half of the table.
@@ -997,7 +1013,6 @@ AttendPlan attend_plan(int64_t T, int64_t B, int64_t max_q, int64_t Hq, int64_t 
     if (own)
         a.splits_o = a.wide_o ? attend_wide_splits(a.tiles_o * Hkv * B, rows_o, len_o, T * Hq * D, bytes_p)
                               : attend_splits(a.tiles_o * Hkv * B, len_o);
-    a.few_rows = (a.wide_p || prefix_len == 0 || rows_p <= 8) && (a.wide_o || rows_o <= 8);
     const int64_t slots = a.splits_p + a.splits_o;
     a.direct = slots == 1;
     if (!a.direct) {
@@ -1061,7 +1076,7 @@ mfp8_status launch_attend(attend::Params p, const AttendPlan& plan, int dev, cud
         p.tiles_o = plan.wide_o ? 0 : int(plan.tiles_o);
         p.beside = wide > 0;
         const dim3 grid(unsigned(narrow + (wide > 0)));
-        st = plan.few_rows ? launch_pdl(attend::attend_rows_kernel<D, 8>, grid, attend::kThreads, stream, L8::SMEM, p)
+        st = plan.row_tile == 8 ? launch_pdl(attend::attend_rows_kernel<D, 8>, grid, attend::kThreads, stream, L8::SMEM, p)
                            : launch_pdl(attend::attend_rows_kernel<D, 16>, grid, attend::kThreads, stream, L16::SMEM, p);
         if (st != MFP8_OK) return st;
     }
