@@ -37,7 +37,7 @@
 // byte permutes.  The probabilities change sides by 8 x 8 transposes.
 //
 // 256 sequences with 128 to 4096 own tokens (8 KV heads of 128, 1.1 GB), the
-// tall kernel beside on 32 SMs: 218 us in all, 5.2 TB/s, 0.79 of the copy
+// tall kernel beside on 32 SMs: 220 us in all, 5.1 TB/s, 0.78 of the copy
 // rate; two blocks of four warps per SM, bound by the instructions of few
 // warps (query rows as matrix rows, 16 to a tile: 265 us).  Three blocks with
 // two stages 232 us, with four stages of 16 tokens 240, four blocks with three
@@ -234,13 +234,15 @@ attend_rows_kernel(const Params p) {
     extern __shared__ __align__(128) uint8_t smem[];
     grid_launch_dependents();
     // Beside the tall kernel there is nothing to wait for: its blocks let this
-    // grid start once they have waited themselves, so all that came before is
-    // there, and the two write different slots.  One block more than there is
-    // work waits for the tall kernel, so that this grid ends after it and
+    // grid start once they have waited themselves, so all that came before has
+    // ended (the fence keeps what this SM's L1 held before that out of sight),
+    // and the two write different slots.  One block more than there is work
+    // waits for the tall kernel, so that this grid ends after it and
     // join_kernel, which waits for this grid, sees both.
     const bool waits = p.beside && blockIdx.x == gridDim.x - 1;
     if (!p.beside || waits) grid_dependency_wait();
     if (waits) return;
+    if (p.beside) __threadfence();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
 
