@@ -404,7 +404,7 @@ MFP8_API mfp8_status mfp8_rope_kv_store(const void* QKV_bf16, int64_t ldqkv, int
 /* Kernel choice for mfp8_prefix_attention. */
 typedef enum {
     MFP8_ATTEND_AUTO = 0, /* chosen for the prefix and for the own tokens from their sizes */
-    MFP8_ATTEND_ROWS = 1, /* 16 query rows per KV head at a time: bound by reading the cache */
+    MFP8_ATTEND_ROWS = 1, /* 8 or 16 query rows per KV head at a time: bound by reading the cache */
     MFP8_ATTEND_TALL = 2  /* up to 256 at a time on the tcgen05 tensor cores */
 } mfp8_attend_path;
 
