@@ -546,14 +546,14 @@ attend_rows_kernel(const Params p) {
             sum += __shfl_xor_sync(0xffffffffu, sum, 4);
             sum += __shfl_xor_sync(0xffffffffu, sum, 8);
             sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-            const float inv = sum > 0.0f ? ldexpf(1.0f / sum, vexp - 127 - 14) : 0.0f;
+            const float inv = sum != 0.0f ? ldexpf(1.0f / sum, vexp - 127 - 14) : 0.0f;
             const int i0 = warp * ROWS + nb * 8 + 2 * c + j;
             float4* dst = reinterpret_cast<float4*>(om + i0 * L::OPITCH + g * NT);
 #pragma unroll
             for (int i = 0; i < NT / 2; i += 2)
                 dst[i / 2] = make_float4(o[nb][i][j] * inv, o[nb][i][2 + j] * inv, o[nb][i + 1][j] * inv,
                                          o[nb][i + 1][2 + j] * inv);
-            if (g == 0) lm[i0] = sum > 0.0f ? m[nb][j] + log2f(sum) : -INFINITY;
+            if (g == 0) lm[i0] = sum != 0.0f ? m[nb][j] + log2f(sum) : -INFINITY;
         }
     __syncthreads();
     constexpr int CPT = ROWS * D / kThreads;  // values per thread, all of one row
@@ -567,8 +567,8 @@ attend_rows_kernel(const Params p) {
     float wt[kWarps], sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sum += wt[w] = ex2(lm[w * ROWS + i] - mz);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    const float out_lse = sum > 0.0f ? mx + log2f(sum) : -INFINITY;
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+    const float out_lse = sum != 0.0f ? mx + log2f(sum) : -INFINITY;
     const int64_t row = int64_t(k.tok0 + r / p.G) * p.Hq + h * p.G + r % p.G;
     float y[CPT];
 #pragma unroll
@@ -668,14 +668,14 @@ join_kernel(const Params p) {
             }
         }
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + row * D + lane * VPL);
 #pragma unroll
     for (int j = 0; j < VPL; j += 2) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(y[j] * inv, y[j + 1] * inv);
         dst[j / 2] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    if (lane == 0 && p.lse) p.lse[row] = sum > 0.0f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+    if (lane == 0 && p.lse) p.lse[row] = sum != 0.0f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 }  // namespace attend

@@ -475,7 +475,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         if (!both && side == 1 && ok) ok = wait_asleep(bar(L::OFULL), 0, abort_flag);  // every MMA is done
         tc_fence_after();
         // l carries 2^kNorm, O that and 2^kVNorm / M
-        const bool any = ok && m > -INFINITY;
+        const bool any = ok && (m > -INFINITY || l != l);  // a NaN stays one
         const float inv = any ? ldexpf(1.0f / l, vexp - 127 - kVNorm) : 0.0f;
         float my_lse = any ? m + (log2f(l) - float(kNorm)) : -INFINITY;
         float* buf = reinterpret_cast<float*>(smem + L::Q_OFF);  // [D][128]: side 1's output when joined
@@ -497,7 +497,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             named_bar_sync(1, 256);
             const float other = lbuf[i];
             const float mxl = fmaxf(my_lse, other);
-            if (mxl == -INFINITY) {
+            if (my_lse == -INFINITY && other == -INFINITY) {
                 w0 = 0.0f;
             } else {
                 w0 = ex2(my_lse - mxl);

@@ -228,6 +228,40 @@ def test_layers_in_a_row_with_both_kernels(n, own, P, Hq):
         assert all(torch.equal(x, y) for x, y in zip(bufs, want)), k
 
 
+def test_two_streams_at_once_with_both_kernels():
+    batches = [Batch([1] * 80, [9, 700] * 40, 6000, 8, 2, 128, 64, seed=21),
+               Batch([1] * 70, [300, 40] * 35, 3000, 16, 4, 64, 32, seed=22)]
+    want = [run(b)[0] for b in batches]
+    for b, w in zip(batches, want):
+        b.check(*run(b))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in batches]
+    got = [[], []]
+    for _ in range(6):
+        for i, s in enumerate(streams):
+            got[i].append(run(batches[i], stream=s)[0])
+    torch.cuda.synchronize()
+    for w, outs in zip(want, got):
+        assert all(torch.equal(w, o) for o in outs)
+
+
+@pytest.mark.parametrize("path", (mfp8.ATTEND_AUTO,) + PATHS)
+def test_a_row_with_nan_leaves_the_others_alone(path):
+    def run(x):
+        return mfp8.prefix_attention(*x.args(), want_lse=True, path=path) + (x.D ** -0.5,)
+
+    b = Batch([1] * 80, [9, 700] * 40, 6000, 8, 2, 128, 64, seed=23)
+    want, _, _ = run(b)
+    b.q[17].fill_(math.nan)
+    b.q[40, 3] = math.inf
+    got, lse, _ = run(b)
+    assert got[17].isnan().all() and got[40, 3].isnan().all() and lse[17].isnan().all()
+    keep = torch.ones(80, 8, dtype=torch.bool, device="cuda")
+    keep[17] = False
+    keep[40, 3] = False
+    assert torch.equal(got[keep], want[keep])
+
+
 @pytest.mark.parametrize("path", PATHS)
 def test_lengths_and_pages_out_of_range_are_cut_and_reported(path):
     def run(x):
