@@ -247,24 +247,24 @@ attend_rows_kernel(const Params p) {
     const int g = lane >> 2, c = lane & 3;
 
     // ---- which rows, which tokens
-    int64_t u = blockIdx.x;
-    const int64_t np = int64_t(p.tiles_p) * p.splits_p * p.Hkv;
+    uint32_t u = blockIdx.x;  // the host keeps grids below 2^31
+    const uint32_t np = uint32_t(p.tiles_p * p.splits_p * p.Hkv), heads = uint32_t(p.Hkv);
     int split, h, tile;
     Task k;
     if (u < np) {
-        h = int(u % p.Hkv);
-        u /= p.Hkv;
-        split = int(u % p.splits_p);
-        tile = int(u / p.splits_p);
+        h = int(u % heads);
+        u /= heads;
+        split = int(u % uint32_t(p.splits_p));
+        tile = int(u / uint32_t(p.splits_p));
         k = prefix_task(p);
     } else {
         u -= np;
-        h = int(u % p.Hkv);
-        u /= p.Hkv;
-        split = int(u % p.splits_o);
-        u /= p.splits_o;
-        tile = int(u % p.tiles_o);
-        k = own_task(p, int(u / p.tiles_o));
+        h = int(u % heads);
+        u /= heads;
+        split = int(u % uint32_t(p.splits_o));
+        u /= uint32_t(p.splits_o);
+        tile = int(u % uint32_t(p.tiles_o));
+        k = own_task(p, int(u / uint32_t(p.tiles_o)));
     }
     const int nrows = k.n * p.G;
     const int r0 = tile * ROWS;
@@ -614,7 +614,7 @@ join_kernel(const Params p) {
     const int64_t rows = int64_t(p.T) * p.Hq;
     const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
     if (row >= rows) return;
-    const int t = int(row / p.Hq);
+    const int t = int(uint32_t(row) / uint32_t(p.Hq));  // T * Hq < 2^31
     if (t < p.q_start[0] || t >= p.q_start[p.B]) return;
     const int slots = p.splits_p + p.splits_o;
     constexpr int VPL = D / 32;     // values per lane
