@@ -19,7 +19,9 @@
 // own tokens: G rows per KV head), where a 128-row tcgen05 tile would be
 // almost empty.  e4m3 codes are exact in f16.  Q goes to f16 with a power of two per
 // row that puts its largest element in [2^7, 2^8): exact for elements down
-// to 2^-22 of that largest, off by at most 2^-33 of it below.  The
+// to 2^-24 of that largest, off by at most 2^-32 of it below.  A row with an
+// infinity or NaN is NaN in every place: its logits are (some of its products
+// are infinite or NaN, so whatever it sees, its softmax has no value).  The
 // probabilities times the value scales go to f16 relative to the largest
 // value scale seen (a power of two M per warp): p sv / M 2^14, 11 bits down
 // to 2^-28 of M.  Sums, maxima and outputs stay in fp32.
@@ -208,6 +210,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 // magnitude's bf16 bits (tiny rows are taken as 2^-119).
 __device__ __forceinline__ int row_exponent(uint32_t amax_bits) { return max(int(amax_bits >> 7), 8) - 127 - 7; }
 
+// 2^-e, which a row is multiplied by; NaN for a row that holds an infinity or NaN.
+__device__ __forceinline__ float row_factor(int e, uint32_t amax_bits) {
+    return amax_bits < 0x7f80u ? pow2i(-e) : __int_as_float(0x7fc00000);
+}
+
 template <int D, int ROWS>
 struct RowsLayout {
     static constexpr int CHUNKS = D / 16;                 // 16-byte pieces of a code row
@@ -362,7 +369,7 @@ attend_rows_kernel(const Params p) {
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         const int e = row_exponent(amax);
-        const float m = pow2i(-e);
+        const float m = row_factor(e, amax);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             qf[nb][i][0] = pack_f16x2(bf16_lo(w[i][0]) * m, bf16_hi(w[i][0]) * m);

@@ -13,10 +13,12 @@
 //               cores as they are.  Q is the sum of two e4m3 terms: bf16 has
 //               8 significant bits, e4m3 has 4, so with q scaled by a power
 //               of two per row, hi = e4m3(q) and lo = e4m3(q - hi) hold q
-//               exactly down to 2^-10 of the row's largest element (which
+//               exactly down to 2^-9.8 of the row's largest element (which
 //               lies in [224, 448]) and are off by at most 2^-17.8 of it
 //               below.  Two e4m3 products cost what one f16 product costs,
-//               and no key is ever converted.
+//               and no key is ever converted.  A row with an infinity or
+//               NaN is NaN in every place (e4m3 has no infinity: converted,
+//               one would become a finite 896).
 //   p           z sk_j (fp32) to e^(z - m), m lagging behind the running
 //               maximum by up to kLag octaves, so O is rescaled only when
 //               the maximum has grown by more; p 2^kNorm goes to f16.
@@ -367,7 +369,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             // 2^e puts the largest element in [224, 448]: its exponent at 8, or at 7 above 1.75 * 2^n
             int e = max(int(amax >> 7), 10) - 127 - 8;
             if ((amax & 0x7fu) > 0x60u) ++e;
-            const float m = pow2i(-e);
+            const float m = row_factor(e, amax);
             f = fmaxf(p.scale_log2 * pow2i(e), kFltMin);
             const uint32_t hi = sb + L::Q_OFF + side * 2 * L::QB + i * D, lo = hi + L::QB;
             const uint32_t x = D == 128 ? uint32_t(i & 7) : uint32_t((i >> 1) & 3);
