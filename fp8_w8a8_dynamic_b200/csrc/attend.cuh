@@ -99,6 +99,7 @@ struct Params {
 struct Task {
     int tok0;    // first token of the sequence (or batch)
     int n;       // its tokens
+    int cut;     // tokens behind those, past max_q, that the grid has no tiles for
     int len;     // cached tokens
     int offset;  // row r sees tokens below offset + r / G (own) or len (prefix)
     bool prefix;
@@ -111,6 +112,7 @@ __device__ __forceinline__ Task prefix_task(const Params& p) {
     const int q0 = min(max(p.q_start[0], 0), p.T);
     k.tok0 = q0;
     k.n = min(max(p.q_start[p.B], q0), p.T) - q0;
+    k.cut = 0;
     k.len = p.prefix_len;
     k.offset = p.prefix_len;
     k.prefix = true;
@@ -129,8 +131,9 @@ __device__ __forceinline__ Task own_task(const Params& p, int b) {
     const int most = int(min(int64_t(p.max_pages) << p.ps_shift, kMaxTokens));
     k.tok0 = q0;
     k.n = min(q1 - q0, p.max_q);
+    k.cut = q1 - q0 - k.n;
     k.len = min(max(l, 0), most);
-    if (a != q0 || e != q1 || k.n != q1 - q0 || l != k.len) record_device_status(MFP8_ERR_INDEX);
+    if (a != q0 || e != q1 || k.cut != 0 || l != k.len) record_device_status(MFP8_ERR_INDEX);
     k.offset = k.len - (q1 - q0) + 1;
     k.prefix = false;
     k.pages = p.table + int64_t(b) * p.ld_table;
@@ -141,6 +144,25 @@ __device__ __forceinline__ Task own_task(const Params& p, int b) {
 
 __device__ __forceinline__ int visible(const Task& k, int token) {
     return k.prefix ? k.len : min(k.len, k.offset + token);
+}
+
+// Row r of the task in Q's order of rows, KV head h.
+__device__ __forceinline__ int64_t row_of(const Params& p, const Task& k, int h, int r) {
+    return int64_t(k.tok0 + r / p.G) * p.Hq + h * p.G + r % p.G;
+}
+
+// Rows r0 .. r1 - 1 of KV head h see nothing of this slot's tokens.  Whole block.
+template <int D>
+__device__ __forceinline__ void nothing_seen(const Params& p, const Task& k, int h, int slot, int r0, int r1) {
+    for (int r = r0 + int(threadIdx.x); r < r1; r += int(blockDim.x)) {
+        const int64_t row = row_of(p, k, h, r);
+        if (!p.direct) p.part_lse[int64_t(slot) * p.T * p.Hq + row] = -INFINITY;
+        else if (p.lse) p.lse[row] = -INFINITY;
+    }
+    if (p.direct)
+        for (int64_t i = threadIdx.x; i < int64_t(r1 - r0) * (D / 8); i += blockDim.x)
+            reinterpret_cast<uint4*>(p.O)[row_of(p, k, h, r0 + int(i / (D / 8))) * (D / 8) + i % (D / 8)] =
+                make_uint4(0u, 0u, 0u, 0u);
 }
 
 // Page index of token `tok` of the task, checked against the pool.
@@ -275,6 +297,9 @@ attend_rows_kernel(const Params p) {
     }
     const int nrows = k.n * p.G;
     const int r0 = tile * ROWS;
+    const int slot = k.slot0 + split;
+    // Every slot of a row has to hold something when join_kernel reads it: query tokens past max_q see the prefix alone.
+    if (tile == 0 && k.cut > 0) nothing_seen<D>(p, k, h, slot, nrows, nrows + k.cut * p.G);
     if (r0 >= nrows) return;
     const int rlast = min(r0 + ROWS, nrows) - 1;
     const int seen = max(visible(k, rlast / p.G), 0);  // of the tile's last row, which sees most
@@ -282,26 +307,7 @@ attend_rows_kernel(const Params p) {
     int chunk = (k.len + k.splits - 1) / k.splits;
     chunk = max((chunk + kWarps * kIter - 1) / (kWarps * kIter) * (kWarps * kIter), kMinChunk);
     const int64_t first = int64_t(split) * chunk;
-    const int slot = k.slot0 + split;
-    if (first >= seen) {  // nothing here
-        for (int i = threadIdx.x; i < ROWS; i += kThreads) {
-            const int r = r0 + i;
-            if (r < nrows) {
-                const int64_t row = int64_t(k.tok0 + r / p.G) * p.Hq + h * p.G + r % p.G;
-                if (!p.direct) p.part_lse[int64_t(slot) * p.T * p.Hq + row] = -INFINITY;
-                else if (p.lse) p.lse[row] = -INFINITY;
-            }
-        }
-        if (p.direct)
-            for (int i = threadIdx.x; i < ROWS * (D / 8); i += kThreads) {
-                const int r = r0 + i / (D / 8);
-                if (r < nrows) {
-                    const int64_t row = int64_t(k.tok0 + r / p.G) * p.Hq + h * p.G + r % p.G;
-                    reinterpret_cast<uint4*>(p.O)[row * (D / 8) + i % (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
-                }
-            }
-        return;
-    }
+    if (first >= seen) return nothing_seen<D>(p, k, h, slot, r0, rlast + 1);
     const int k0 = int(first), k1 = min(k0 + chunk, seen);
     const int iters = (k1 - k0 + kIter - 1) / kIter;
 
@@ -576,7 +582,7 @@ attend_rows_kernel(const Params p) {
     for (int w = 0; w < kWarps; ++w) sum += wt[w] = ex2(lm[w * ROWS + i] - mz);
     const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
     const float out_lse = sum != 0.0f ? mx + log2f(sum) : -INFINITY;
-    const int64_t row = int64_t(k.tok0 + r / p.G) * p.Hq + h * p.G + r % p.G;
+    const int64_t row = row_of(p, k, h, r);
     float y[CPT];
 #pragma unroll
     for (int j = 0; j < CPT; ++j) y[j] = 0.0f;

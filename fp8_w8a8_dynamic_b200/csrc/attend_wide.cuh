@@ -286,6 +286,8 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         tc_fence_after();
         if (warp == 13) tmem_dealloc(*tmem_holder, 512);
     };
+    const int slot = k.slot0 + split;
+    if (pair == 0 && k.cut > 0) nothing_seen<D>(p, k, h, slot, nrows, nrows + k.cut * p.G);
     if (r0 >= nrows) return leave();
     const bool both = nrows - r0 > kTile;  // the sides hold different rows
     const int rlast = min(r0 + kWideRows, nrows) - 1;
@@ -293,18 +295,9 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
     int chunk = (k.len + k.splits - 1) / k.splits;
     chunk = max((chunk + kTile - 1) / kTile * kTile, kTile);
     const int64_t first = int64_t(split) * chunk;
-    const int slot = k.slot0 + split;
     const int64_t all_rows = int64_t(p.T) * p.Hq;
-    auto row_of = [&](int r) { return int64_t(k.tok0 + r / p.G) * p.Hq + h * p.G + r % p.G; };
-    if (first >= seen) {  // nothing here
-        for (int r = r0 + int(threadIdx.x); r <= rlast; r += kWideThreads) {
-            if (!p.direct) p.part_lse[int64_t(slot) * all_rows + row_of(r)] = -INFINITY;
-            else if (p.lse) p.lse[row_of(r)] = -INFINITY;
-        }
-        if (p.direct)
-            for (int i = threadIdx.x; i < (rlast - r0 + 1) * (D / 8); i += kWideThreads)
-                reinterpret_cast<uint4*>(p.O)[row_of(r0 + i / (D / 8)) * (D / 8) + i % (D / 8)] =
-                    make_uint4(0u, 0u, 0u, 0u);
+    if (first >= seen) {
+        nothing_seen<D>(p, k, h, slot, r0, rlast + 1);
         return leave();
     }
     const int k0 = int(first), k1 = min(k0 + chunk, seen);
@@ -471,7 +464,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             if (lane == 0) mbar_arrive(bar(L::PFULL + side));
         }
         // ---- the output of this side's tiles
-        const int64_t my_row = live ? row_of(r) : 0;
+        const int64_t my_row = live ? row_of(p, k, h, r) : 0;
         const int mine = both ? nt : (nt + 1 - side) / 2;
         bool ok = mine > 0 && n == mine && wait_asleep(bar(L::OFULL + side), 0, abort_flag);
         if (!both && side == 1 && ok) ok = wait_asleep(bar(L::OFULL), 0, abort_flag);  // every MMA is done

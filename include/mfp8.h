@@ -428,7 +428,8 @@ MFP8_API size_t mfp8_prefix_attention_workspace_bytes(int64_t T, int64_t B, int6
  *   q_start [B + 1] int32, not decreasing, within 0 .. T; kv_len [B] int32.
  *       Tokens outside q_start[0] .. q_start[B] - 1 are left as they were in
  *       O_bf16 and lse.
- *   max_q: no sequence has more query tokens (max_q >= 1).
+ *   max_q: no sequence has more query tokens (max_q >= 1; any past it see the
+ *       prefix alone).
  *   k_pages, k_scale, v_pages, v_scale: as mfp8_kv_page_store writes them.
  *   prefix_pages [ceil(prefix_len / page_size)] int32: the prefix's pages in
  *       order (NULL when prefix_len is 0).

@@ -1,5 +1,6 @@
 """Attention over a shared prefix where a row, a cached token or a length is
 not as it should be, on the GPU against the 64-bit form."""
+import copy
 import math
 
 import pytest
@@ -64,3 +65,47 @@ def test_an_infinite_row_that_sees_nothing(path):
     out, lse, scale = run(b, path)
     b.check(out, lse, scale)
     assert (out[:2] == 0).all() and (lse[:2] == -math.inf).all()
+
+
+# ------------------------------------------ more query tokens than `max_q` --
+
+def cut_ref(b, max_q, scale):
+    """(out, out bound, lse, lse bound) when query tokens past max_q of their sequence see the prefix alone."""
+    c = copy.copy(b)
+    c.own, c.slots = [0] * b.B, [b.slots[0]] + [b.slots[0][:0]] * b.B
+    late = torch.zeros(b.T, dtype=torch.bool, device="cuda")
+    for i in range(b.B):
+        late[b.start[i] + max_q:b.start[i + 1]] = True
+    full, alone = b.ref(scale), c.ref(scale)
+    return late, [torch.where(late.view((-1,) + (1,) * (x.dim() - 1)), y, x) for x, y in zip(full, alone)]
+
+
+@pytest.mark.parametrize("path", ALL_PATHS)
+@pytest.mark.parametrize("n,own,P,D", [([3, 9, 2], [20, 40, 8], 0, 64), ([3, 9, 2], [700, 40, 3000], 0, 128),
+                                       ([3, 9, 2], [20, 40, 8], 90, 128), ([40, 1, 300], [60, 5, 900], 3000, 64)])
+def test_query_tokens_past_max_q(n, own, P, D, path):
+    """They see the prefix alone, whatever the workspace holds, and are
+    reported; the others are not disturbed."""
+    b = Batch(n, own, P, 8, 2, D, 16, seed=P + D, first_row=2, extra_rows=1)
+    max_q = 4
+    b.max_q = max_q
+    size = mfp8.mfp8_prefix_attention_workspace_bytes(b.T, b.B, max_q, 8, 2, D, P, b.page_table.shape[1], 16)
+    outs = []
+    for fill in (1.0, math.nan, -3.0e38):
+        ws = torch.full((max(size, 16) // 4,), fill, device="cuda")
+        out = torch.full((b.T, 8, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        out, lse, scale = run(b, path, workspace=ws, out=out)
+        assert mfp8.device_status() == mfp8.ERR_INDEX
+        outs.append((out, lse))
+    late, (ref, tol, rl, lt) = cut_ref(b, max_q, scale)
+    assert late.any()
+    for out, lse in outs:
+        assert (out[:2] == 7.0).all() and (out[-1:] == 7.0).all()
+        rows = slice(b.start[0], b.start[-1])
+        assert torch.equal(out[rows], outs[0][0][rows]) and torch.equal(lse[rows], outs[0][1][rows])
+    o, r, t = out[rows].double(), ref[rows], tol[rows]
+    assert ((o - r).abs() <= t).all()
+    none = torch.isinf(rl[rows])
+    assert torch.equal(none, lse[rows] == -math.inf)
+    assert ((lse[rows].double() - rl[rows]).abs()[~none] <= lt[rows][~none]).all()
+    assert (o[none] == 0).all() and bool(none.any()) == (P == 0)
