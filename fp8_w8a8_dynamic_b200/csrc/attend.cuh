@@ -122,24 +122,48 @@ __device__ __forceinline__ Task prefix_task(const Params& p) {
     return k;
 }
 
-// Device lengths that do not fit what the call said are cut and reported.
+// A sequence's place among the query tokens and its cached tokens, cut to
+// what the call said and reported when they do not fit it.
+struct Lengths {
+    int q0, q1;  // its query tokens
+    int n;       // of them, those the grid has tiles for
+    int len;     // cached tokens
+};
+__device__ __forceinline__ Lengths lengths_of(const int32_t* q_start, const int32_t* kv_len, int b, int T, int max_q,
+                                              int most) {
+    Lengths x;
+    const int a = q_start[b], e = q_start[b + 1], l = kv_len[b];
+    x.q0 = min(max(a, 0), T);
+    x.q1 = min(max(e, x.q0), T);
+    x.n = min(x.q1 - x.q0, max_q);
+    x.len = min(max(l, 0), most);
+    if (a != x.q0 || e != x.q1 || x.n != x.q1 - x.q0 || l != x.len) record_device_status(MFP8_ERR_INDEX);
+    return x;
+}
+
 __device__ __forceinline__ Task own_task(const Params& p, int b) {
+    const Lengths x = lengths_of(p.q_start, p.kv_len, b, p.T, p.max_q, int(min(int64_t(p.max_pages) << p.ps_shift, kMaxTokens)));
     Task k;
-    const int a = p.q_start[b], e = p.q_start[b + 1], l = p.kv_len[b];
-    const int q0 = min(max(a, 0), p.T);
-    const int q1 = min(max(e, q0), p.T);
-    const int most = int(min(int64_t(p.max_pages) << p.ps_shift, kMaxTokens));
-    k.tok0 = q0;
-    k.n = min(q1 - q0, p.max_q);
-    k.cut = q1 - q0 - k.n;
-    k.len = min(max(l, 0), most);
-    if (a != q0 || e != q1 || k.cut != 0 || l != k.len) record_device_status(MFP8_ERR_INDEX);
-    k.offset = k.len - (q1 - q0) + 1;
+    k.tok0 = x.q0;
+    k.n = x.n;
+    k.cut = x.q1 - x.q0 - x.n;
+    k.len = x.len;
+    k.offset = k.len - (x.q1 - x.q0) + 1;
     k.prefix = false;
     k.pages = p.table + int64_t(b) * p.ld_table;
     k.slot0 = p.splits_p;
     k.splits = p.splits_o;
     return k;
+}
+
+// A call without own tokens has no block that reads a sequence's lengths:
+// they are checked all the same, by the first `threads` threads of each block.
+// Not inlined: that spills in the tall kernel (prompts 680 -> 702 us).
+__device__ __noinline__ void check_lengths(const int32_t* q_start, const int32_t* kv_len, int B, int T, int max_q,
+                                           int threads) {
+    if (int(threadIdx.x) >= threads) return;
+    for (int64_t b = int64_t(blockIdx.x) * threads + threadIdx.x; b < B; b += int64_t(gridDim.x) * threads)
+        lengths_of(q_start, kv_len, int(b), T, max_q, 0);
 }
 
 __device__ __forceinline__ int visible(const Task& k, int token) {
@@ -272,6 +296,7 @@ attend_rows_kernel(const Params p) {
     if (!p.beside || waits) grid_dependency_wait();
     if (waits) return;
     if (p.beside) __threadfence();
+    if (p.splits_o == 0) check_lengths(p.q_start, p.kv_len, p.B, p.T, p.max_q, kThreads);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
 

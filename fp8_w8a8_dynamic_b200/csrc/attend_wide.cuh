@@ -259,6 +259,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
     }
     grid_dependency_wait();
     grid_launch_dependents();
+    if (p.splits_o == 0) check_lengths(p.q_start, p.kv_len, p.B, p.T, p.max_q, 32);
 
     // ---- which rows, which tokens (uniform over the CTA)
     int64_t u = blockIdx.x;

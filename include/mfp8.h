@@ -435,7 +435,7 @@ MFP8_API size_t mfp8_prefix_attention_workspace_bytes(int64_t T, int64_t B, int6
  *       order (NULL when prefix_len is 0).
  *   page_table: B rows ld_table apart of max_pages int32: each sequence's
  *       own pages in order; entries past its last token are not read.  NULL
- *       when max_pages is 0.  kv_len[b] is at most max_pages * page_size.
+ *       when max_pages is 0 (no own tokens: every kv_len[b] is 0).  kv_len[b] is at most max_pages * page_size.
  *       The work is cut by max_pages, so a table as narrow as the longest
  *       sequence is the fastest.
  *   softmax_scale finite and > 0 (up to 2e38).

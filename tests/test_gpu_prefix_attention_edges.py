@@ -109,3 +109,26 @@ def test_query_tokens_past_max_q(n, own, P, D, path):
     assert torch.equal(none, lse[rows] == -math.inf)
     assert ((lse[rows].double() - rl[rows]).abs()[~none] <= lt[rows][~none]).all()
     assert (o[none] == 0).all() and bool(none.any()) == (P == 0)
+
+
+# ------------------------------------------------------ a prefix and no table --
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("B", (3, 200))
+def test_lengths_without_a_page_table_are_checked(B, path):
+    """Starts past the last token or decreasing, own tokens without a table,
+    and more query tokens than max_q are reported where nothing but the prefix
+    is read; the rows they do not concern keep their bits."""
+    b = Batch([1] * B, [0] * B, 70, 8, 2, 64, 16, seed=B)
+    want, want_lse, scale = run(b, path)
+    b.check(want, want_lse, scale)
+    assert mfp8.device_status() == mfp8.OK
+    start, none = b.q_start.clone(), b.kv_len.clone()
+    for where, at, value in (("q_start", B, B + 5), ("q_start", 0, -1), ("q_start", 1, 0), ("q_start", B - 1, 0), ("q_start", B - 2, B),
+                             ("kv_len", B - 1, 1), ("kv_len", 0, -4)):
+        getattr(b, where)[at] = value
+        out, lse, _ = run(b, path)
+        assert mfp8.device_status() == mfp8.ERR_INDEX, (where, at, value)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        b.q_start.copy_(start)
+        b.kv_len.copy_(none)
