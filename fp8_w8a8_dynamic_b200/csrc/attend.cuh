@@ -26,6 +26,13 @@
 // value scale seen (a power of two M per warp): p sv / M 2^14, 11 bits down
 // to 2^-28 of M.  Sums, maxima and outputs stay in fp32.
 //
+// A value row with an infinity or NaN (mfp8_kv_page_store gives it a scale of
+// NaN) would reach every query row of a matrix instruction, since 0 NaN = NaN:
+// a later token's would spoil the queries before it.  So such rows are taken
+// as zeros, and the first of them is remembered: the rows that see it (a row
+// sees all tokens up to its last) get NaN at the end.  Their log-sum-exp,
+// which the values have no part in, stays what it is.
+//
 // Each warp streams its own share of the chunk, 32 tokens at a time, through
 // a ring of three cp.async stages of its own, so warps never wait for one
 // another until they merge at the end.  Tokens (for z) and dimensions (for
@@ -65,6 +72,7 @@ constexpr int kStages = 3;
 constexpr int kMinChunk = kWarps * kIter * 2;  // tokens: below two iterations per warp a split costs more than it saves
 constexpr int64_t kMaxTokens = int64_t(1) << 30;  // of one sequence
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint32_t kNotFinite = 0x7f800000u;  // a scale's bits from here on: infinity, NaN
 
 struct Params {
     const __nv_bfloat16* Q;
@@ -232,6 +240,7 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000); }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -258,7 +267,7 @@ __device__ __forceinline__ int row_exponent(uint32_t amax_bits) { return max(int
 
 // 2^-e, which a row is multiplied by; NaN for a row that holds an infinity or NaN.
 __device__ __forceinline__ float row_factor(int e, uint32_t amax_bits) {
-    return amax_bits < 0x7f80u ? pow2i(-e) : __int_as_float(0x7fc00000);
+    return amax_bits < 0x7f80u ? pow2i(-e) : quiet_nan();
 }
 
 template <int D, int ROWS>
@@ -427,6 +436,7 @@ attend_rows_kernel(const Params p) {
     float m[NB][2], l[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.0f;
+    int bad_at = INT32_MAX;  // first token of this warp's whose value row is not finite
     int vexp = 27;  // biased exponent just above the largest value scale seen, at least 2^-100
 
     for (int it = warp; it < iters; it += kWarps) {
@@ -486,7 +496,24 @@ attend_rows_kernel(const Params p) {
             }
         }
         // largest value scale of the iteration's tokens, as a power of two above it
-        const uint32_t svb = __reduce_max_sync(0xffffffffu, __float_as_uint(ld_shared_f32(scales + kIter * 4 + lane * 4)));
+        const uint32_t svl = __float_as_uint(ld_shared_f32(scales + kIter * 4 + lane * 4));
+        uint32_t svb = __reduce_max_sync(0xffffffffu, svl);
+        if (svb >= kNotFinite) {  // value rows that are not finite are taken out: zeros, with a scale of zero
+            const bool bad = svl >= kNotFinite;
+            if (bad) {
+#pragma unroll 1
+                for (int i = 0; i < L::CHUNKS; ++i) st_shared_v4(st + kIter * D + lane * D + i * 16, 0u, 0u, 0u, 0u);
+                st_shared_u32(scales + kIter * 4 + lane * 4, 0u);
+            }
+            bad_at = min(bad_at, base + __ffs(int(__ballot_sync(0xffffffffu, bad))) - 1);
+            svb = __reduce_max_sync(0xffffffffu, bad ? 0u : svl);
+            __syncwarp();
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const uint32_t at = scales + kIter * 4 + (t * 16 + g) * 4;
+                sv[t][0] = ld_shared_f32(at), sv[t][1] = ld_shared_f32(at + 32);
+            }
+        }
         const int ve = max(vexp, min(int(svb >> 23) + 1, 254));
         const float vadj = pow2i(max(vexp - ve, -126));
         const float vnorm = pow2i(14 - (ve - 127));
@@ -584,7 +611,8 @@ attend_rows_kernel(const Params p) {
             sum += __shfl_xor_sync(0xffffffffu, sum, 4);
             sum += __shfl_xor_sync(0xffffffffu, sum, 8);
             sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-            const float inv = sum != 0.0f ? ldexpf(1.0f / sum, vexp - 127 - 14) : 0.0f;
+            float inv = sum != 0.0f ? ldexpf(1.0f / sum, vexp - 127 - 14) : 0.0f;
+            if (lim[nb][j] > bad_at) inv = quiet_nan();
             const int i0 = warp * ROWS + nb * 8 + 2 * c + j;
             float4* dst = reinterpret_cast<float4*>(om + i0 * L::OPITCH + g * NT);
 #pragma unroll
@@ -688,21 +716,23 @@ join_kernel(const Params p) {
     for (int j = 0; j < VPL; ++j) y[j] = 0.0f;
     for (int s0 = 0; s0 < slots; s0 += 32) {
         if (s0 > 0) lse0 = s0 + lane < slots ? p.part_lse[int64_t(s0 + lane) * rows + row] : -INFINITY;
-        const float w = ex2(lse0 - mz);
+        // -1: a slot that holds no output.  (A weight may be 0 for another reason, and its output NaN.)
+        const float w = lse0 == -INFINITY ? -1.0f : ex2(lse0 - mz);
         const int n = min(32, slots - s0);
         for (int i0 = 0; i0 < n; i0 += kAhead) {
             float wi[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 wi[i] = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
-                if (i0 + i >= n) wi[i] = 0.0f;
-                if (s0 + i0 > 0 && wi[i] > 0.0f) load(s0 + i0 + i, v[i]);
+                if (i0 + i >= n) wi[i] = -1.0f;
+                if (s0 + i0 > 0 && !(wi[i] < 0.0f)) load(s0 + i0 + i, v[i]);
             }
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
+                if (wi[i] < 0.0f) continue;
                 sum += wi[i];
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) y[j] = wi[i] > 0.0f ? fmaf(wi[i], v[i][j], y[j]) : y[j];
+                for (int j = 0; j < VPL; ++j) y[j] = fmaf(wi[i], v[i][j], y[j]);
             }
         }
     }

@@ -220,13 +220,27 @@ __device__ __forceinline__ float mask_logits(uint32_t (&z)[128], int base, int l
 }
 
 // log2 of M, biased: a power of two above `before` and above the value scales
-// (in shared memory at `sv`) of the tile's `valid` tokens.  Whole warp.
-__device__ __forceinline__ int tile_vexp(int before, uint32_t sv, int valid, int lane) {
+// (in shared memory at `sv`) of the tile's `valid` tokens.  Value rows that are
+// not finite do not count; `bad_at` becomes the first of them (the tile starts
+// at token `base`) if it is smaller.  Whole warp.
+__device__ __forceinline__ int tile_vexp(int before, uint32_t sv, int valid, int lane, int base, int& bad_at) {
     uint32_t top = 0;
 #pragma unroll
     for (int q = 0; q < kTile / 32; ++q)
         if (lane + 32 * q < valid) top = max(top, __float_as_uint(ld_shared_f32(sv + (lane + 32 * q) * 4)));
-    return max(before, min(int(__reduce_max_sync(0xffffffffu, top) >> 23) + 1, 254));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (top >= kNotFinite) {
+        uint32_t finite = 0, first = kTile;
+#pragma unroll 1
+        for (int t = lane; t < valid; t += 32) {
+            const uint32_t s = __float_as_uint(ld_shared_f32(sv + t * 4));
+            if (s < kNotFinite) finite = max(finite, s);
+            else first = min(first, uint32_t(t));
+        }
+        top = __reduce_max_sync(0xffffffffu, finite);
+        bad_at = min(bad_at, base + int(__reduce_min_sync(0xffffffffu, first)));
+    }
+    return max(before, min(int(top >> 23) + 1, 254));
 }
 
 // Which part and unit of the grid a CTA works on.
@@ -395,7 +409,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         const uint32_t lane_base = tmem + ((warp & 3u) << 21);
         const uint32_t tS = lane_base + uint32_t(side) * 128u, tO = lane_base + 256u + uint32_t(side) * 128u;
         float m = -INFINITY, l = 0.0f;
-        int vexp = kMinVexp, n = 0;
+        int vexp = kMinVexp, n = 0, bad_at = INT32_MAX;
         const uint64_t f2 = pack2(f, f);
         for (int j = side; j < steps; j += 2, ++n) {
             const int tile = both ? j >> 1 : j;
@@ -403,7 +417,7 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             const int base = k0 + tile * kTile;
             if (!wait_asleep(bar(L::LFULL + ls), (tile / L::SST) & 1, abort_flag)) break;
             const uint32_t sk = sb + L::S_OFF + ls * 1024;
-            const int ve = tile_vexp(vexp, sk + 512, min(kTile, k1 - base), lane);
+            const int ve = tile_vexp(vexp, sk + 512, min(kTile, k1 - base), lane, base, bad_at);
             if (!wait_asleep(bar(L::SFULL + side), n & 1, abort_flag)) break;
             tc_fence_after();
             uint32_t z[128];
@@ -472,7 +486,8 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
         tc_fence_after();
         // l carries 2^kNorm, O that and 2^kVNorm / M
         const bool any = ok && (m > -INFINITY || l != l);  // a NaN stays one
-        const float inv = any ? ldexpf(1.0f / l, vexp - 127 - kVNorm) : 0.0f;
+        float inv = any ? ldexpf(1.0f / l, vexp - 127 - kVNorm) : 0.0f;
+        if (lim > bad_at) inv = quiet_nan();
         float my_lse = any ? m + (log2f(l) - float(kNorm)) : -INFINITY;
         float* buf = reinterpret_cast<float*>(smem + L::Q_OFF);  // [D][128]: side 1's output when joined
         float* lbuf = reinterpret_cast<float*>(smem + L::LSE_OFF);
@@ -567,7 +582,8 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
             const int ls = tile % L::SST;
             if (!wait_asleep(bar(L::LFULL + ls), (tile / L::SST) & 1, abort_flag)) break;
             const uint32_t sc = sb + L::S_OFF + ls * 1024;
-            const int ve = tile_vexp(vexp[both ? 0 : tile & 1], sc + 512, valid, lane);
+            int bad_at = INT32_MAX;
+            const int ve = tile_vexp(vexp[both ? 0 : tile & 1], sc + 512, valid, lane, 0, bad_at);
             vexp[both ? 0 : tile & 1] = ve;
             const float inv = pow2i(kVNorm + 127 - ve);
 #pragma unroll 4
@@ -575,8 +591,10 @@ attend_wide_kernel(const Params p, const WideGrid wg, const __grid_constant__ CU
                 const int row = a * RPI + tid / CH;
                 const uint32_t x = D == 128 ? uint32_t(row & 7) : uint32_t((row >> 1) & 3);
                 uint4 v = lds128(src + row * D + ((uint32_t(ch) ^ x) << 4));
-                float s = ld_shared_f32(sc + 512 + row * 4) * inv;
-                if (row >= valid) v = make_uint4(0u, 0u, 0u, 0u), s = 0.0f;  // whatever the page holds there, NaN too
+                const float sv = ld_shared_f32(sc + 512 + row * 4);
+                float s = sv * inv;
+                // whatever the page holds past the end, NaN too; value rows that are not finite
+                if (row >= valid || __float_as_uint(sv) >= kNotFinite) v = make_uint4(0u, 0u, 0u, 0u), s = 0.0f;
                 const __half2 s2 = __float2half2_rn(s);
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 uint32_t o[8];

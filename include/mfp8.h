@@ -423,7 +423,9 @@ MFP8_API size_t mfp8_prefix_attention_workspace_bytes(int64_t T, int64_t B, int6
  * With G = Hq / Hkv, row (t, h) reads KV head h / G:
  *   z = softmax_scale * (q . K) over the tokens it sees,
  *   out = sum e^(z - lse) V,  lse = ln sum e^z;  K, V = dec(code) * scale.
- * A row that sees nothing gets zeros and lse = -inf.
+ * A row that sees nothing gets zeros and lse = -inf.  An infinity or NaN in a
+ * query row or in a key row that it sees makes its outputs and lse NaN, one in
+ * a value row that it sees its outputs; other rows are not touched by it.
  *   Q_bf16: T tokens ldq elements apart, each Hq rows of D.
  *   q_start [B + 1] int32, not decreasing, within 0 .. T; kv_len [B] int32.
  *       Tokens outside q_start[0] .. q_start[B] - 1 are left as they were in

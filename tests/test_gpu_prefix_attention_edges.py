@@ -132,3 +132,68 @@ def test_lengths_without_a_page_table_are_checked(B, path):
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
         b.q_start.copy_(start)
         b.kv_len.copy_(none)
+
+
+# --------------------------------------- cached tokens that are not finite --
+
+SPOILT = {  # n, own, P, D, [(sequence or -1 for the prefix, token)]
+    "in the middle of a prompt": ([40, 3], [60, 20], 100, 128, [(0, 47)]),
+    "a prompt's last token": ([40, 3], [60, 20], 0, 64, [(0, 59)]),
+    "two in a long prompt": ([300], [900], 0, 128, [(0, 700), (0, 893)]),
+    "in a short prompt and a long one": ([300, 20, 70], [700, 20, 300], 555, 64, [(1, 11), (2, 299), (0, 410)]),
+    "before the prompt": ([30, 30], [200, 40], 0, 128, [(0, 3)]),
+    "a decode step": ([1] * 5, [50, 700, 3, 9, 1], 20, 128, [(1, 655), (4, 0)]),
+    "in the prefix": ([1, 4], [50, 9], 300, 64, [(-1, 131)]),
+}
+
+
+@pytest.mark.parametrize("path", ALL_PATHS)
+@pytest.mark.parametrize("what", (math.inf, -math.inf, math.nan))
+@pytest.mark.parametrize("side", ("value", "key"))
+@pytest.mark.parametrize("name", SPOILT)
+def test_cached_tokens_that_are_not_finite(name, side, what, path):
+    """A value row that holds an infinity or NaN makes NaN the outputs of the
+    rows that see it and of no others, those of its tile and page among them;
+    the log-sum-exps, which have no values in them, stay.  A key row makes
+    both NaN."""
+    n, own, P, D, spots = SPOILT[name]
+    Hq, Hkv, ps, head = 8, 2, 16, 1
+    b = Batch(n, own, P, Hq, Hkv, D, ps, seed=len(name))
+    pages, scale = (b.v_pages, b.v_scale) if side == "value" else (b.k_pages, b.k_scale)
+    slots = torch.stack([b.slots[1 + q][t] for q, t in spots]).cuda()
+    x = torch.randn((len(spots), Hkv, D), generator=torch.Generator("cuda").manual_seed(1), device="cuda").bfloat16()
+    mfp8.kv_page_store(x, slots, pages, scale)
+    ref, tol, rl, lt = b.ref(D ** -0.5)
+    x[:, head, 7] = what
+    mfp8.kv_page_store(x, slots, pages, scale)  # the other heads' bytes stay as they were
+    out, lse, _ = run(b, path)
+    sees = torch.zeros(b.T, Hq, dtype=torch.bool, device="cuda")
+    for q, t in spots:
+        for s in range(b.B) if q < 0 else [q]:
+            first = 0 if q < 0 else max(0, t - (own[s] - n[s]))
+            sees[b.start[s] + first:b.start[s + 1], head * Hq // Hkv:(head + 1) * Hq // Hkv] = True
+    assert sees.any()
+    assert out[sees].isnan().all()
+    assert ((out.double() - ref).abs() <= tol)[~sees].all()
+    fine = ~sees if side == "key" else torch.ones_like(sees)
+    assert ((lse.double() - rl).abs() <= lt)[fine].all() and lse[~fine].isnan().all()
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_a_value_that_is_not_finite_under_no_weight(path):
+    """A token whose weight is far below the smallest number still counts: 0 NaN is NaN, whatever slot it is in."""
+    b = Batch([1, 1], [3000, 3000], 3000, 8, 2, 128, 16, seed=41)
+    q = torch.zeros_like(b.q)
+    q[..., 0] = 100.0
+    b.q = q
+    k = torch.zeros((1, 2, 128), dtype=torch.bfloat16, device="cuda")
+    for s, t, z in ((0, 5, 100.0), (1, 2000, -100.0), (2, 2000, -100.0)):
+        k[..., 0] = z
+        mfp8.kv_page_store(k, b.slots[s][t:t + 1].cuda(), b.k_pages, b.k_scale)
+    out, lse, _ = run(b, path)
+    assert out.isfinite().all() and lse.isfinite().all()
+    at = b.slots[1][2000]
+    b.v_scale[at // 16, 0, at % 16] = math.nan
+    out, lse2, _ = run(b, path)
+    assert out[0, :4].isnan().all() and out[0, 4:].isfinite().all() and out[1].isfinite().all()
+    assert torch.equal(lse2, lse)
