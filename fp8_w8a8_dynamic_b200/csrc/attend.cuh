@@ -197,9 +197,11 @@ __device__ __forceinline__ void nothing_seen(const Params& p, const Task& k, int
                 make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Page index of token `tok` of the task, checked against the pool.
+// Page index of token `tok` of the task, checked against the pool.  An
+// ordinary load: the kernel before this one may have written the table, and no
+// fence orders the read-only path.
 __device__ __forceinline__ int page_of(const Params& p, const Task& k, int tok, int last) {
-    const int pg = __ldg(k.pages + (min(tok, last) >> p.ps_shift));
+    const int pg = k.pages[min(tok, last) >> p.ps_shift];
     if (uint32_t(pg) >= uint64_t(p.n_pages)) {
         record_device_status(MFP8_ERR_INDEX);
         return 0;
@@ -297,10 +299,11 @@ attend_rows_kernel(const Params p) {
     grid_launch_dependents();
     // Beside the tall kernel there is nothing to wait for: its blocks let this
     // grid start once they have waited themselves, so all that came before has
-    // ended (the fence keeps what this SM's L1 held before that out of sight),
-    // and the two write different slots.  One block more than there is work
-    // waits for the tall kernel, so that this grid ends after it and
-    // join_kernel, which waits for this grid, sees both.
+    // ended and its writes are performed, and the two write different slots.
+    // What this SM's L1 held before that is kept out of sight by the fence,
+    // since nothing here is read as constant (page_of).  One block more than
+    // there is work waits for the tall kernel, so that this grid ends after it
+    // and join_kernel, which waits for this grid, sees both.
     const bool waits = p.beside && blockIdx.x == gridDim.x - 1;
     if (!p.beside || waits) grid_dependency_wait();
     if (waits) return;

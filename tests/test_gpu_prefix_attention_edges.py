@@ -197,3 +197,94 @@ def test_a_value_that_is_not_finite_under_no_weight(path):
     out, lse2, _ = run(b, path)
     assert out[0, :4].isnan().all() and out[0, 4:].isfinite().all() and out[1].isfinite().all()
     assert torch.equal(lse2, lse)
+
+
+# ------------------------------------------------------ decode steps in a row --
+
+@pytest.mark.parametrize("update", ("before the store", "after the store"))
+@pytest.mark.parametrize("P,Hq", [(6000, 8), (1500, 32)])  # own tokens in 8-row and in 16-row tiles beside a tall prefix
+def test_decode_steps_in_a_row(P, Hq, update):
+    """Steps of rope_kv_store and prefix_attention whose two kernels run beside
+    each other: each step writes new tokens next to cached ones, lengthens the
+    sequences and gives some a new page right before the attention that needs
+    them.  The bits of the same steps with a synchronisation after every call,
+    eager and replayed, and the last step against 64 bits."""
+    Hkv, D, ps, steps = 2, 128, 64, 6
+    own = [9, 61, 62, 700] * 20
+    B = len(own)
+    b = Batch([1] * B, own, P, Hq, Hkv, D, ps, seed=P, spare_pages=2 * B, max_pages=12)
+    free = sorted(set(range(b.k_pages.shape[0])) - set(b.prefix_pages.tolist())
+                  - set(b.page_table[b.page_table >= 0].tolist()))
+    tables, slots, table = [], [], b.page_table.clone()
+    for s in range(steps):
+        rows = []
+        for i, l in enumerate(own):
+            at = l + s
+            if int(table[i, at // ps]) < 0:
+                table[i, at // ps] = free.pop()
+            rows.append(int(table[i, at // ps]) * ps + at % ps)
+        tables.append(table.clone())
+        slots.append(torch.tensor(rows, device="cuda"))
+    lens = [torch.tensor(own, dtype=torch.int32, device="cuda") + s + 1 for s in range(steps)]
+    pos = [(P + x - 1).contiguous() for x in lens]
+    qkv = [torch.randn((B, (Hq + 2 * Hkv) * D), device="cuda", generator=torch.Generator("cuda").manual_seed(s)).bfloat16()
+           for s in range(steps)]
+    freq, _ = mfp8.rope_frequencies(D, 5e6)
+    start = [x.clone() for x in (b.k_pages, b.k_scale, b.v_pages, b.v_scale, b.page_table, b.kv_len)]
+    outs = [torch.zeros((B, Hq, D), dtype=torch.bfloat16, device="cuda") for _ in range(steps)]
+    size = mfp8.mfp8_prefix_attention_workspace_bytes(B, B, 1, Hq, Hkv, D, P, 12, ps)
+    ws = torch.zeros((size,), dtype=torch.uint8, device="cuda")
+
+    def decode(state, outs, ws, between):
+        kp, ks, vp, vs, table, kv_len = state
+        for s in range(steps):
+            if update == "before the store":
+                table.copy_(tables[s])
+                kv_len.add_(1)
+                between()
+            q = mfp8.rope_kv_store(qkv[s], Hq, pos[s], freq, slots[s], kp, ks, vp, vs)
+            between()
+            if update == "after the store":
+                table.copy_(tables[s])
+                kv_len.add_(1)
+                between()
+            mfp8.prefix_attention(q, b.q_start, kv_len, table, b.prefix_pages, P, kp, ks, vp, vs, 1, out=outs[s],
+                                  workspace=ws)
+            between()
+        return q
+
+    def apart():
+        state = [x.clone() for x in start]
+        ys = [torch.zeros_like(x) for x in outs]
+        q = decode(state, ys, torch.zeros_like(ws), torch.cuda.synchronize)
+        return q, ys, state
+
+    def same(state, ys, want):
+        assert all(torch.equal(x, y) for x, y in zip(ys, want[1]))
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(state, want[2]))
+
+    want = apart()
+    live = [x.clone() for x in start]
+    decode(live, outs, ws, lambda: None)
+    same(live, outs, want)
+
+    last = copy.copy(b)
+    last.q = want[0]
+    last.k_pages, last.k_scale, last.v_pages, last.v_scale, last.page_table, last.kv_len = want[2]
+    last.own = [l + steps for l in own]
+    last.slots = [b.slots[0]] + [torch.cat([sl, torch.stack([x[i] for x in slots]).cpu()])
+                                 for i, sl in enumerate(b.slots[1:])]
+    last.check(outs[-1], None, D ** -0.5)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        decode(live, outs, ws, lambda: None)
+    for k in range(4):
+        for x in qkv:
+            x.mul_(-0.5 if k % 2 else -2.0)
+        want = apart()
+        for x, y in zip(live, start):
+            x.copy_(y)
+        ws.fill_(255)
+        graph.replay()
+        same(live, outs, want)
