@@ -880,13 +880,15 @@ mfp8_status launch_rope(rope::Params p, int layout, cudaStream_t stream) {
     const int tpb = rope::kThreads >> shift;
     const dim3 grid(unsigned((p.T + tpb - 1) / tpb));
     const int smem = tpb * p.rot * int(sizeof(float));
-    // Rows per thread and pass: two or three, whichever divides a thread's rows
-    // with fewer passes to spare (32 heads of 128: two, 48: three; one pass of
-    // three instead of two passes of two is 71 us instead of 75 in the fused
-    // store of 16384 tokens, two of two instead of three 43 instead of 46 in
-    // the rotation alone).
+    // Rows per thread and pass: three where that divides a thread's rows and
+    // two does not (no pass with places to spare), else two.  Both ways, us for
+    // two / three rows, rotation alone and fused store, 134 MB of head rows of
+    // 128: 2 rows 41.6 / 44.0 and 54.0 / 57.6; 3 rows 42.8 / 41.4 and 50.3 /
+    // 47.5; 4 rows 42.0 / 42.7 and 45.7 / 48.9; 5 rows 41.8 / 42.6 and 46.4 /
+    // 46.2; 6 rows 42.3 / 43.2 and 44.2 / 43.7; 8 rows 42.8 / 44.1 and 44.7 /
+    // 45.3 (heads of 256 the same).
     const int rows = (heads * upr + (1 << shift) - 1) >> shift;
-    const bool three = rows > 2 && rows != 4;
+    const bool three = rows % 3 == 0 && rows % 2 != 0;
     const bool il = layout == MFP8_ROPE_INTERLEAVED;
     auto run = [&](auto kern) { return launch_pdl(kern, grid, rope::kThreads, stream, smem, p); };
     auto pick = [&](auto u) {
