@@ -45,13 +45,14 @@
 // dimensions each of four value rows, whose bytes are paired by token with
 // byte permutes.  The probabilities change sides by 8 x 8 transposes.
 //
-// 256 sequences with 128 to 4096 own tokens (8 KV heads of 128, 1.1 GB), the
-// tall kernel beside on 32 SMs: 220 us in all, 5.1 TB/s, 0.78 of the copy
-// rate; two blocks of four warps per SM, bound by the instructions of few
-// warps (query rows as matrix rows, 16 to a tile: 265 us).  Three blocks with
-// two stages 232 us, with four stages of 16 tokens 240, four blocks with three
-// stages of 16 tokens 228; for 64 sequences of up to 1024 these take 75 us
-// instead of 78.
+// 256 sequences with 128 to 4096 own tokens (8 KV heads of 128, 1.1 GB) behind
+// 8192 shared ones: 222 us in all, 5.1 TB/s, 0.78 of the copy rate.  Such own
+// tokens alone, 187 us for 1.16 GB, 0.94 of it: the difference is the tall
+// kernel, whose 32 CTAs hold their SMs for about 165 us, and the join's 10.
+// Two blocks of four warps per SM; before (query rows as matrix rows, 16 to a
+// tile) 265 us.  When that step took 220, three blocks with two stages took
+// 232, with four stages of 16 tokens 240, four blocks with three stages of 16
+// tokens 228; for 64 sequences of up to 1024 these took 75 us instead of 78.
 #pragma once
 
 #include <cstdint>

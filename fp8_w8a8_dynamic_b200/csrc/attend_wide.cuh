@@ -43,13 +43,16 @@
 // units, and a step takes 2300 (1.17 us): a side's tile goes through 1900 to
 // 2200 cycles of softmax, 1024 of MMAs and two hand-overs (a commit, the
 // waiting warp's wake-up and its arrive back take 490 to 560 cycles), and only
-// two sides fit in TMEM to overlap them.  Besides the steps a CTA takes about
-// 10 us (Q, the ends of the pipeline, its output).  Measured and not kept,
-// 3000 query tokens of 32 heads over 10007 shared ones (now 645 us, 0.49 of
-// the burst peak): 16 softmax warps 850 us; 64-token steps with two buffers of
-// z per side 1040; four rows per thread in the 16 x 256-bit TMEM layout, a
-// quarter of the scales' shared-memory reads, 790; an issuing lane per side in
-// turns 670; waits that poll without sleeping 1.48 us a step.
+// two sides fit in TMEM to overlap them; P is handed over whole, so P V of a
+// tile starts behind its last exponential.  Besides the steps a CTA takes about
+// 10 us (Q, the ends of the pipeline, its output), and a grid that ends in part
+// of a wave leaves SMs idle: 3000 query tokens of 32 heads over 10007 shared
+// ones are 376 CTAs, 2.54 waves on 148 SMs, 640 us, 0.49 of the burst peak;
+// their steps spread evenly would take 500.  Measured and not kept there: 16
+// softmax warps 850 us; 64-token steps with two buffers of z per side 1040;
+// four rows per thread in the 16 x 256-bit TMEM layout, a quarter of the
+// scales' shared-memory reads, 790; an issuing lane per side in turns 670;
+// waits that poll without sleeping 1.48 us a step.
 //
 // Every wait is bounded (wait_asleep), as in the GEMM kernels.
 #pragma once

@@ -920,9 +920,12 @@ struct AttendPlan {
 };
 
 constexpr int kAttendSms = 148;
-// Blocks per SM that the row kernel's splits aim at: 64 sequences of up to
-// 1024 own tokens took 78 us in all with 4 and with 6, 82 with 8; 256 of up
-// to 4096: 218, 219, 217.
+// Blocks per SM that the row kernel's splits aim at.  Sequences x own tokens
+// (8 KV heads of 128), us for 2, 4, 8, 16: 4 x 16384 42, 34, 43, 55; 16 x 16384
+// 120, 111, 105, 109; 64 x 64 to 8192 124, 110, 106, 110; 64 x 4096 92, 104,
+// 104, 108; 64 x 1024 32, 40, 43, 50; 256 x 128 to 4096 187 with one slot
+// each (2 to 8), 201.  Sequences of one length want whole waves, uneven ones
+// small pieces; every sequence gets the same number of pieces, whatever its length.
 constexpr int kRowBlocks = 4;
 constexpr int64_t kAttendMax = int64_t(1) << 20;
 
@@ -963,7 +966,12 @@ int attend_splits(int64_t units, int64_t len) {
 // bytes of cache, is read meanwhile by the SMs that the tall kernel leaves
 // free, then by all; a slot's outputs are written and joined at 4 TB/s.  64
 // sequences over 32768 shared tokens (8 units), slots and us: 12 86, 14 77, 16
-// 78, 18 79; 256 over 8192 (32 units), 1 218, 2 228, 3 232, 4 237.
+// 78, 18 79; 256 over 8192 (32 units), 1 218, 2 228, 3 232, 4 237.  Elsewhere,
+// the choice in brackets: 32 sequences with 500 own tokens over 65536, 9 99,
+// 14 71, [18 73]; 128 over 16384, 4 99, 6 85, [8 92], 9 91; heads of 64, 64
+// over 32768, 9 79, 14 61, [16 64]; 256 over 8192 without own tokens, 3 84,
+// [4 80], 6 86; 3010 prompt tokens over 10007, [1 625], 2 688; one prompt of
+// 8192, [1 672], 2 815; of 700, [1 26], 2 31.
 int attend_wide_splits(int64_t units, int64_t rows, int64_t len, int64_t out_values, double beside) {
     constexpr double kStepUs = 1.2, kFree = 45e3, kFull = 5.4e6;  // bytes per us: one SM of a few, all
     const int64_t tiles = (len + attend::kTile - 1) / attend::kTile;

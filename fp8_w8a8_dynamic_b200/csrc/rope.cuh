@@ -30,8 +30,11 @@
 // shared memory, behind the first loads.  Rotating 16384 tokens of 32 x 128
 // values (268 MB) took 79 us with a vector per thread and shuffles between
 // the halves (75% of the issue slots busy), 52 us with two vectors per thread
-// at 80 registers, 43 us at 64 (6.2 TB/s); 48 registers spill and take 62 us.
-// The fused store of 16384 tokens of 32 + 8 + 8 rows (370 MB): 117, 86, 71 us.
+// at 80 registers, 43 us at 64 (6.2 TB/s), 62 us at 48.  At 64 every build
+// spills a little: the half layout 44 bytes out and 40 in with two rows per
+// pass, 100 and 216 with three.  The fused store of 16384 tokens of 32 + 8 + 8
+// rows (370 MB; three rows): 117, 86, 71 us.  Lanes and rows are powers of two:
+// 20 heads of 96 use 120 of 256 places in two passes, 36 heads of 64 144 of 256.
 #pragma once
 
 #include <cstdint>

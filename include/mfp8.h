@@ -440,7 +440,8 @@ MFP8_API size_t mfp8_prefix_attention_workspace_bytes(int64_t T, int64_t B, int6
  *       when max_pages is 0 (no own tokens: every kv_len[b] is 0).  kv_len[b] is at most max_pages * page_size.
  *       The work is cut by max_pages, so a table as narrow as the longest
  *       sequence is the fastest.
- *   softmax_scale finite and > 0 (up to 2e38).
+ *   softmax_scale finite and > 0 (up to 2e38); logits have to be finite in
+ *       fp32.
  *   O_bf16 [T][Hq][D]; lse [T][Hq] fp32 or NULL (written).  Neither may
  *       overlap an input.
  *   workspace: mfp8_prefix_attention_workspace_bytes(...) bytes, any
