@@ -288,3 +288,37 @@ def test_decode_steps_in_a_row(P, Hq, update):
         ws.fill_(255)
         graph.replay()
         same(live, outs, want)
+
+
+# ----------------------------------------------------------- what is written --
+
+@pytest.mark.parametrize("path", ALL_PATHS)
+@pytest.mark.parametrize("max_q", (2, 9))  # cuts the prompt of 9, or fits
+@pytest.mark.parametrize("P,own", [(0, [20, 40, 8]), (90, [20, 40, 8]), (3000, [700, 40, 3000]), (700, [0, 0, 0])])
+def test_nothing_else_is_written(P, own, max_q, path):
+    """Outputs, log-sum-exps and workspace between guards: rows outside the
+    batch and everything around the buffers keep their bytes."""
+    D, Hq, Hkv, ps = 128, 8, 2, 16
+    b = Batch([3, 9, 2], own, P, Hq, Hkv, D, ps, seed=P, first_row=2, extra_rows=3)
+    table = b.page_table if b.page_table.shape[1] else None
+    pages = 0 if table is None else table.shape[1]
+    need = mfp8.mfp8_prefix_attention_workspace_bytes(b.T, b.B, max_q, Hq, Hkv, D, P, pages, ps)
+    sizes = (b.T * Hq * D * 2, b.T * Hq * 4, need)
+    bufs = [torch.full((n + 8192,), 0xa5, dtype=torch.uint8, device="cuda") for n in sizes]
+    q = b.q.contiguous()
+    status = mfp8.mfp8_prefix_attention(
+        q.data_ptr(), Hq * D, b.T, Hq, Hkv, D, b.q_start.data_ptr(), b.kv_len.data_ptr(), b.B, max_q,
+        b.k_pages.data_ptr(), b.k_scale.data_ptr(), b.v_pages.data_ptr(), b.v_scale.data_ptr(), b.k_pages.shape[0], ps,
+        b.prefix_pages.data_ptr() if P else None, P, None if table is None else table.data_ptr(), pages, pages, 0.1,
+        bufs[0].data_ptr() + 4096, bufs[1].data_ptr() + 4096, bufs[2].data_ptr() + 4096, need, path)
+    assert status == mfp8.OK
+    assert mfp8.device_status() == (mfp8.ERR_INDEX if max_q == 2 else mfp8.OK)
+    for x, n in zip(bufs, sizes):
+        assert (x[:4096] == 0xa5).all() and (x[4096 + n:] == 0xa5).all()
+    for x, row in zip(bufs[:2], (Hq * D * 2, Hq * 4)):
+        rows = x[4096:4096 + b.T * row].view(b.T, row)
+        assert (rows[:2] == 0xa5).all() and (rows[-3:] == 0xa5).all()
+        assert not (rows[2:-3] == 0xa5).all(-1).any()
+    if max_q == 9:
+        b.check(bufs[0][4096:4096 + sizes[0]].view(torch.bfloat16).view(b.T, Hq, D),
+                bufs[1][4096:4096 + sizes[1]].view(torch.float32).view(b.T, Hq), 0.1)
